@@ -385,6 +385,96 @@ lpgemm_status lpgemm_pack_int4(const int8_t *logical, uint8_t *packed, int64_t r
 lpgemm_status lpgemm_unpack_int4(const uint8_t *packed, int8_t *logical, int64_t rows, int64_t K,
                                  hipStream_t stream);
 
+/* ---- microscaled 4-bit floating point (mxfp4) -----------------------------
+ *
+ * The OCP microscaling format with 4-bit elements: a row of K values is cut
+ * into blocks of 32 consecutive values; every value is an e2m1 code (0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6 and their negatives; sign in bit 3) and every block has
+ * one e8m0 scale byte s standing for 2^(s - 127), 255 for NaN:
+ *     value(k) = e2m1(code(k)) * 2^(s(k / 32) - 127)
+ * A row holds U = ceil(K / 128) units, 64 code bytes and 4 scale bytes each:
+ *     codes   [rows][64 U]   element k in byte k / 2, even k in the low nibble
+ *     scales  [rows][4 U]    block j in byte j
+ * Codes past K are zero, and so every value past K is; a block that lies past
+ * K has scale 127.  With K % 128 == 0 there is no padding.
+ * Codes are 16-byte aligned, scales 4-byte aligned, D 16-byte aligned and
+ * other values to their element (LPGEMM_ERR_INVALID_ARG otherwise).
+ */
+#define LPGEMM_MXFP4_MAX_K (1 << 20)
+#define LPGEMM_MXFP4_MAX_ROWS (1 << 30)   /* of D, A and B (each group's) */
+#define LPGEMM_MXFP4_MAX_GROUPS 1024
+
+/*
+ * Rows of F32, BF16 or F16 values -> codes and scales.
+ *   X       device, x_dtype [rows][K], row r at X + r * ldx elements
+ *           (ldx >= K; any alignment of the element size)
+ *   codes, scales   device, written whole, the padding of each row included
+ * With a = max |x| of a block, s = max(floor(log2 a) - 2, -127) + 127 (a = 0:
+ * s = 0) and code = the e2m1 value nearest to x / 2^(s - 127), a tie going to
+ * the even code, magnitudes above 6 becoming 6.  A block that holds a NaN or
+ * an infinity gets s = 255 and zero codes: all its values become NaN.
+ * LPGEMM_ERR_INVALID_ARG for negative sizes, another x_dtype, ldx < K with
+ * several rows, a null or misaligned pointer; LPGEMM_ERR_UNSUPPORTED for K
+ * above LPGEMM_MXFP4_MAX_K.
+ */
+lpgemm_status lpgemm_mxfp4_quantize(const void *X, lpgemm_out_dtype x_dtype, int64_t ldx, uint8_t *codes,
+                                    uint8_t *scales, int64_t rows, int64_t K, hipStream_t stream);
+
+/*
+ * Codes and scales -> the values they stand for, y_dtype [rows][K] dense.
+ * Exact for F32 and BF16 (every value has at most two significant bits);
+ * F16 rounds to nearest even.  Errors as for lpgemm_mxfp4_quantize.
+ */
+lpgemm_status lpgemm_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, void *Y, lpgemm_out_dtype y_dtype,
+                                      int64_t rows, int64_t K, hipStream_t stream);
+
+/*
+ * D[m][n] = out( sum_k a(m,k) b(n,k) )   of mxfp4 operands
+ *   A, SFA   device, codes and scales of M rows of K values
+ *   B, SFB   device, codes and scales of N rows of K values
+ *   D        device, [M][N] F32, BF16 or F16, written
+ * Products of one block are exact; the matrix cores add them in groups of 8 k
+ * (each group exact: its products are multiples of 1/4 of at most 36, times
+ * one power of two) and the groups to a binary32 accumulator, rounding to
+ * nearest even; partial sums of K ranges, where a kernel takes them, are added
+ * in binary32 in a fixed order.  So |D - S| <= 1.01 (K / 8 + 16) 2^-24 P before
+ * out(), with S the exact sum and P = sum |a b|, while no scale product leaves
+ * binary32's normal range.  A block of scale 255 makes its row (A) or column
+ * (B) of D NaN.  K == 0 writes zeros.
+ * lpgemm_mxfp4_workspace_size gives the bytes of scratch memory that a call
+ * can use to split K over more workgroups; the workspace is 256-byte aligned,
+ * and with less than that, or none (null, 0), the call runs without.
+ * LPGEMM_ERR_INVALID_ARG for negative sizes, another out_dtype, a null or
+ * misaligned pointer that would be dereferenced; LPGEMM_ERR_UNSUPPORTED above
+ * the limits; LPGEMM_ERR_HIP if a launch failed.
+ */
+lpgemm_status lpgemm_mxfp4(const uint8_t *A, const uint8_t *SFA, const uint8_t *B, const uint8_t *SFB, void *D,
+                           lpgemm_out_dtype out_dtype, int64_t M, int64_t N, int64_t K, void *workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+lpgemm_status lpgemm_mxfp4_workspace_size(int64_t M, int64_t N, int64_t K, int32_t cu_count, size_t *bytes);
+
+/*
+ * The product of every group of rows with that group's matrix: for row i of D
+ * in group e, offsets[e] <= i < offsets[e + 1],
+ *     D[i][n] = out( sum_k a(rows[i], k) b_e(n, k) )
+ *   A, SFA    device, codes and scales of T rows
+ *   rows      device, int32 [R], the row of A for each row of D, or null (row
+ *             i is row i; T == R).  An index outside [0, T) stands for a row
+ *             of zeros.  With rows, A's codes span at most 2^31 - 1 bytes.
+ *   B, SFB    device, codes and scales of E matrices of N rows, one after another
+ *   offsets   device, int32 [E + 1], non-decreasing from 0 to R; groups may be
+ *             empty.  Read on the device, so a call needs no synchronisation.
+ *             Each offset is taken into [0, R] and a decreasing pair is an
+ *             empty group, so nothing outside D is written; rows of D in no
+ *             group are left as they are.
+ *   D         device, [R][N], written
+ * Accuracy and errors as for lpgemm_mxfp4; E above LPGEMM_MXFP4_MAX_GROUPS
+ * is LPGEMM_ERR_UNSUPPORTED.
+ */
+lpgemm_status lpgemm_mxfp4_grouped(const uint8_t *A, const uint8_t *SFA, int64_t T, const int32_t *rows,
+                                   const uint8_t *B, const uint8_t *SFB, int64_t E, const int32_t *offsets, void *D,
+                                   lpgemm_out_dtype out_dtype, int64_t R, int64_t N, int64_t K, hipStream_t stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char *lpgemm_status_string(lpgemm_status status);
 

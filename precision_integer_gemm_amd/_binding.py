@@ -32,10 +32,14 @@ EXPORTS = ("lpgemm_int4_int4", "lpgemm_w4a8", "lpgemm_int4_int4_ws", "lpgemm_w4a
            "lpgemm_int4_int4_scaled_ws", "lpgemm_int4_int4_blockscaled", "lpgemm_w4a8_blockscaled",
            "lpgemm_fp8_e4m3", "lpgemm_fp8_e5m2", "lpgemm_pack_int4",
            "lpgemm_unpack_int4", "lpgemm_status_string", "lpgemm_plan",
-           "lpgemm_set_kernel_override")
+           "lpgemm_set_kernel_override", "lpgemm_mxfp4_quantize", "lpgemm_mxfp4_dequantize",
+           "lpgemm_mxfp4", "lpgemm_mxfp4_workspace_size", "lpgemm_mxfp4_grouped")
 SIZE_MAX = 2 ** 64 - 1
 STATIC_SCRATCH_BYTES = 128 << 20  # LPGEMM_STATIC_SCRATCH_BYTES
 WORKSPACE_ALIGN = 256
+# microscaled 4-bit rows: units of 128 values, 64 code bytes and 4 scale bytes
+MXFP4_UNIT, MXFP4_UNIT_CODES, MXFP4_UNIT_SCALES = 128, 64, 4
+MXFP4_MAX_K, MXFP4_MAX_GROUPS = 1 << 20, 1024
 
 
 class LpgemmError(RuntimeError):
@@ -106,6 +110,14 @@ def lib() -> ctypes.CDLL:
         f = getattr(L, name)
         f.argtypes = [p, p, i64, i64, p]
         f.restype = ctypes.c_int
+    L.lpgemm_mxfp4_quantize.argtypes = [p, ctypes.c_int, i64, p, p, i64, i64, p]
+    L.lpgemm_mxfp4_dequantize.argtypes = [p, p, p, ctypes.c_int, i64, i64, p]
+    L.lpgemm_mxfp4.argtypes = [p, p, p, p, p, ctypes.c_int, i64, i64, i64, p, sz, p]
+    L.lpgemm_mxfp4_workspace_size.argtypes = [i64, i64, i64, i32, ctypes.POINTER(sz)]
+    L.lpgemm_mxfp4_grouped.argtypes = [p, p, i64, p, p, p, i64, p, p, ctypes.c_int, i64, i64, i64, p]
+    for name in ("lpgemm_mxfp4_quantize", "lpgemm_mxfp4_dequantize", "lpgemm_mxfp4",
+                 "lpgemm_mxfp4_workspace_size", "lpgemm_mxfp4_grouped"):
+        getattr(L, name).restype = ctypes.c_int
     L.lpgemm_status_string.argtypes = [ctypes.c_int]
     L.lpgemm_status_string.restype = ctypes.c_char_p
     L.lpgemm_plan.argtypes = [ctypes.c_int, p, p, p, i64, i64, i64, sz, i32, ctypes.POINTER(PlanInfo)]
@@ -453,3 +465,141 @@ def lpgemm_unpack_int4(packed, *, out=None, stream=None):
     _raise(lib().lpgemm_unpack_int4(packed.data_ptr(), out.data_ptr(), rows, 2 * half,
                                     _stream_handle(stream)), "lpgemm_unpack_int4")
     return out
+
+
+# ---- microscaled 4-bit floating point ------------------------------------------
+def _units(K: int) -> int:
+    return -(-K // MXFP4_UNIT)
+
+
+def _check_on(t, name: str, dtypes, dim: int, device=None):
+    """A dense tensor of the library's: type, rank, device (`device`: the other operands')."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must be {dim}-D, got shape {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU device, got {t.device}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _check_mx(codes, scales, name: str, dim: int, device=None):
+    """Units per row of an mxfp4 operand."""
+    torch = _torch()
+    _check_on(codes, name, (torch.uint8,), dim, device)
+    _check_on(scales, f"scales of {name}", (torch.uint8,), dim, codes.device)
+    units, rest = divmod(codes.shape[-1], MXFP4_UNIT_CODES)
+    if rest or tuple(scales.shape) != (*codes.shape[:-1], MXFP4_UNIT_SCALES * units):
+        raise ValueError(f"{name} must have shape (..., {MXFP4_UNIT_CODES} U) and its scales (..., {MXFP4_UNIT_SCALES} U), "
+                         f"got {tuple(codes.shape)} and {tuple(scales.shape)}")
+    return units
+
+
+def _mx_out(out, dtype, M, N, device):
+    torch = _torch()
+    if out is None:
+        dtype = dtype or torch.bfloat16
+        return torch.empty((M, N), dtype=dtype, device=device), _out_code(dtype)
+    _check_on(out, "out", (dtype or out.dtype,), 2, device)
+    if tuple(out.shape) != (M, N):
+        raise ValueError(f"out must have shape ({M}, {N}), got {tuple(out.shape)}")
+    return out, _out_code(out.dtype)
+
+
+def lpgemm_mxfp4_quantize(x, *, codes=None, scales=None, stream=None):
+    """Rows of float32, bfloat16 or float16 values [rows, K] -> (codes uint8
+    [rows, 64 U], scales uint8 [rows, 4 U]) with U = ceil(K / 128): e2m1 codes
+    and one e8m0 scale byte per 32 values.  Rows of x may be strided (its last
+    dimension is dense)."""
+    torch = _torch()
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    code = _out_code(x.dtype)
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D, got shape {tuple(x.shape)}")
+    if not x.is_cuda:
+        raise ValueError(f"x must be on a GPU device, got {x.device}")
+    rows, K = x.shape
+    ldx = x.stride(0)
+    if (K > 1 and x.stride(1) != 1) or (rows > 1 and ldx < K):
+        raise ValueError(f"x must be dense along its last dimension, its rows apart: strides {x.stride()}")
+    U = _units(K)
+    for name, t, n in (("codes", codes, MXFP4_UNIT_CODES * U), ("scales", scales, MXFP4_UNIT_SCALES * U)):
+        if t is not None:
+            _check_on(t, name, (torch.uint8,), 2, x.device)
+            if tuple(t.shape) != (rows, n):
+                raise ValueError(f"{name} must have shape ({rows}, {n}), got {tuple(t.shape)}")
+    if codes is None:
+        codes = torch.empty((rows, MXFP4_UNIT_CODES * U), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty((rows, MXFP4_UNIT_SCALES * U), dtype=torch.uint8, device=x.device)
+    _raise(lib().lpgemm_mxfp4_quantize(x.data_ptr(), code, ldx, codes.data_ptr(), scales.data_ptr(), rows, K,
+                                       _stream_handle(stream)), "lpgemm_mxfp4_quantize")
+    return codes, scales
+
+
+def lpgemm_mxfp4_dequantize(codes, scales, K, *, dtype=None, out=None, stream=None):
+    """The values [rows, K] that mxfp4 codes and scales stand for (bfloat16 by
+    default; exact in float32 and bfloat16)."""
+    units = _check_mx(codes, scales, "codes", 2)
+    if K < 0 or _units(K) != units:
+        raise ValueError(f"K={K} does not fit {units} units of {MXFP4_UNIT} values")
+    out, code = _mx_out(out, dtype, codes.shape[0], K, codes.device)
+    _raise(lib().lpgemm_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), out.data_ptr(), code, codes.shape[0], K,
+                                         _stream_handle(stream)), "lpgemm_mxfp4_dequantize")
+    return out
+
+
+def lpgemm_mxfp4_workspace_size(M: int, N: int, K: int, cu_count: int = 0) -> int:
+    """Bytes of workspace an lpgemm_mxfp4 call with these sizes can use (host only)."""
+    n = ctypes.c_size_t(0)
+    _raise(lib().lpgemm_mxfp4_workspace_size(M, N, K, cu_count, ctypes.byref(n)), "lpgemm_mxfp4_workspace_size")
+    return int(n.value)
+
+
+def lpgemm_mxfp4(A, SFA, B, SFB, *, dtype=None, out=None, workspace="auto", stream=None):
+    """D[M,N] = A . B^T of mxfp4 operands (codes [M, 64 U] and [N, 64 U], scales
+    [M, 4 U] and [N, 4 U]) with fp32 accumulation, as bfloat16 (default),
+    float16 or float32; workspace as for lpgemm_int4_int4."""
+    units = _check_mx(A, SFA, "A", 2)
+    if _check_mx(B, SFB, "B", 2, A.device) != units:
+        raise ValueError(f"K mismatch: A has {A.shape[1]} bytes per row, B {B.shape[1]}")
+    M, N, K = A.shape[0], B.shape[0], MXFP4_UNIT * units
+    D, code = _mx_out(out, dtype, M, N, A.device)
+    if isinstance(workspace, str) and workspace == "auto":
+        n = lpgemm_mxfp4_workspace_size(M, N, K)
+        workspace = _torch().empty(n, dtype=_torch().uint8, device=A.device) if n else None
+    ws, nws, _keep = _workspace(workspace, None, M, N, K, True, A.device)
+    _raise(lib().lpgemm_mxfp4(A.data_ptr(), SFA.data_ptr(), B.data_ptr(), SFB.data_ptr(), D.data_ptr(), code, M, N, K,
+                              ws, nws, _stream_handle(stream)), "lpgemm_mxfp4")
+    return D
+
+
+def lpgemm_mxfp4_grouped(A, SFA, B, SFB, offsets, *, rows=None, dtype=None, out=None, stream=None):
+    """The product of each group of rows with its own matrix: row i of the result,
+    offsets[e] <= i < offsets[e + 1], is row rows[i] of A times B[e]^T (rows
+    None: row i; an index outside A's rows stands for zeros).  A codes [T, 64 U],
+    B codes [E, N, 64 U], offsets int32 [E + 1] and rows int32 on the device."""
+    torch = _torch()
+    units = _check_mx(A, SFA, "A", 2)
+    if _check_mx(B, SFB, "B", 3, A.device) != units:
+        raise ValueError(f"K mismatch: A has {A.shape[1]} bytes per row, B {B.shape[2]}")
+    E, N = B.shape[0], B.shape[1]
+    _check_on(offsets, "offsets", (torch.int32,), 1, A.device)
+    if offsets.shape[0] != E + 1:
+        raise ValueError(f"offsets must have {E + 1} entries for {E} groups, got {offsets.shape[0]}")
+    T = R = A.shape[0]
+    if rows is not None:
+        _check_on(rows, "rows", (torch.int32,), 1, A.device)
+        R = rows.shape[0]
+    D, code = _mx_out(out, dtype, R, N, A.device)
+    _raise(lib().lpgemm_mxfp4_grouped(A.data_ptr(), SFA.data_ptr(), T, rows.data_ptr() if rows is not None else None,
+                                      B.data_ptr(), SFB.data_ptr(), E, offsets.data_ptr(), D.data_ptr(), code, R, N,
+                                      MXFP4_UNIT * units, _stream_handle(stream)), "lpgemm_mxfp4_grouped")
+    return D

@@ -2,7 +2,8 @@
 
     python -m precision_integer_gemm_amd.build
 
-compiles csrc/lpgemm_api.hip (which includes every kernel) with hipcc into
+compiles csrc/lpgemm_api.hip (which includes every integer and fp8 kernel) and
+csrc/mxfp4_api.hip (the microscaled 4-bit kernels) with hipcc into
 precision_integer_gemm_amd/_lpgemm.so, next to this file, and the measurement
 probe csrc/ceiling_probe.hip into _ceiling.so (loaded only by bench.py).
 """
@@ -12,10 +13,12 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "lpgemm_api.hip")
+MX_SRC = os.path.join(PKG, "csrc", "mxfp4_api.hip")
 LIB = os.path.join(PKG, "_lpgemm.so")
 PROBE_SRC = os.path.join(PKG, "csrc", "ceiling_probe.hip")
 PROBE_LIB = os.path.join(PKG, "_ceiling.so")
@@ -29,9 +32,9 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found; the HIP library needs ROCm's hipcc")
 
 
-def command(out: str, src: str = SRC) -> list[str]:
+def command(out: str, src: str, *mode: str) -> list[str]:
     return [
-        hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-shared", "-fPIC",
+        hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", *mode, "-fPIC",
         # packed fp32 VALU forms are kept out of the generated code
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
         # the scaled epilogue's roundings are part of its definition: no
@@ -42,21 +45,28 @@ def command(out: str, src: str = SRC) -> list[str]:
     ]
 
 
-def compile_one(src: str, lib: str, verbose: bool) -> None:
-    tmp = lib + ".tmp"
-    proc = subprocess.run(command(tmp, src), capture_output=True, text=True)
+def run(cmd: list[str], what: str, verbose: bool) -> None:
+    proc = subprocess.run(cmd, capture_output=True, text=True)
     noise = "is not a recognized feature for this target"
     msgs = [l for l in (proc.stdout + proc.stderr).splitlines() if noise not in l]
     if proc.returncode != 0:
-        raise RuntimeError(f"hipcc failed on {os.path.basename(src)}:\n" + "\n".join(msgs))
+        raise RuntimeError(f"hipcc failed on {what}:\n" + "\n".join(msgs))
     if verbose and msgs:
         print("\n".join(msgs))
-    os.replace(tmp, lib)
 
 
 def build(verbose: bool = False) -> str:
-    compile_one(SRC, LIB, verbose)
-    compile_one(PROBE_SRC, PROBE_LIB, verbose)
+    objects = [LIB + "." + os.path.basename(src) + ".o" for src in (SRC, MX_SRC)]
+    jobs = [(command(o, src, "-c"), os.path.basename(src)) for o, src in zip(objects, (SRC, MX_SRC))]
+    jobs.append((command(PROBE_LIB + ".tmp", PROBE_SRC, "-shared"), os.path.basename(PROBE_SRC)))
+    with ThreadPoolExecutor(len(jobs)) as pool:
+        for done in [pool.submit(run, cmd, what, verbose) for cmd, what in jobs]:
+            done.result()
+    run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", LIB + ".tmp", *objects], "the library", verbose)
+    for o in objects:
+        os.remove(o)
+    os.replace(PROBE_LIB + ".tmp", PROBE_LIB)
+    os.replace(LIB + ".tmp", LIB)
     return LIB
 
 

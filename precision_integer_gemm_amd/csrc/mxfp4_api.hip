@@ -1,0 +1,171 @@
+// mxfp4_api.hip -- the microscaled 4-bit entry points of the C-ABI: argument
+// checks, kernel selection and launches (contract in include/lpgemm.h).
+#include "lpgemm.h"
+
+#include <algorithm>
+
+#include "gemm_mxfp4.hpp"
+#include "mxfp4_quantize.hpp"
+
+using namespace lpgemm;
+
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b != 0); }
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+lpgemm_status launched() { return hipGetLastError() == hipSuccess ? LPGEMM_OK : LPGEMM_ERR_HIP; }
+
+// lpgemm_out_dtype -> OutFormat; -1 for anything but F32, BF16 and F16.
+int format_of(lpgemm_out_dtype d)
+{
+    switch (d) {
+    case LPGEMM_OUT_F32: return OUT_F32;
+    case LPGEMM_OUT_BF16: return OUT_BF16;
+    case LPGEMM_OUT_F16: return OUT_F16;
+    default: return -1;
+    }
+}
+
+uintptr_t element_bytes(int format) { return format == OUT_F32 ? 4u : 2u; }
+
+// rows x K values to or from codes and scales.
+lpgemm_status check_values(const void *x, const void *codes, const void *scales, int format, int64_t rows, int64_t K)
+{
+    if (format < 0 || rows < 0 || K < 0) return LPGEMM_ERR_INVALID_ARG;
+    if (K > LPGEMM_MXFP4_MAX_K || (K > 0 && rows > (INT64_MAX >> 8) / K)) return LPGEMM_ERR_UNSUPPORTED;
+    if (rows == 0 || K == 0) return LPGEMM_OK;
+    if (x == nullptr || codes == nullptr || scales == nullptr || !aligned(x, element_bytes(format)) ||
+        !aligned(codes, 16) || !aligned(scales, 4))
+        return LPGEMM_ERR_INVALID_ARG;
+    return LPGEMM_OK;
+}
+
+template <int OUT>
+lpgemm_status launch_product(const MxArgs &g, hipStream_t stream)
+{
+    const dim3 grid((unsigned)ceil_div(g.N, 128), (unsigned)std::min<int64_t>(ceil_div(g.R, 32), 65535), (unsigned)g.E);
+    hipLaunchKernelGGL((gemm_mxfp4_simple_kernel<OUT>), grid, dim3(256), 0, stream, g);
+    return launched();
+}
+
+// Sizes and pointers that both products share; R rows of D.
+lpgemm_status check_product(const void *A, const void *SFA, const void *B, const void *SFB, const void *D, int format,
+                            int64_t T, int64_t R, int64_t N, int64_t K, int64_t E)
+{
+    if (format < 0 || T < 0 || R < 0 || N < 0 || K < 0 || E < 0) return LPGEMM_ERR_INVALID_ARG;
+    if (K > LPGEMM_MXFP4_MAX_K || T > LPGEMM_MXFP4_MAX_ROWS || R > LPGEMM_MXFP4_MAX_ROWS || N > LPGEMM_MXFP4_MAX_ROWS)
+        return LPGEMM_ERR_UNSUPPORTED;
+    if (R == 0 || N == 0) return LPGEMM_OK;
+    if (D == nullptr || !aligned(D, 16)) return LPGEMM_ERR_INVALID_ARG;
+    if (K > 0 && ((T > 0 && (A == nullptr || SFA == nullptr)) || (E > 0 && (B == nullptr || SFB == nullptr)) ||
+                  !aligned(A, 16) || !aligned(B, 16) || !aligned(SFA, 4) || !aligned(SFB, 4)))
+        return LPGEMM_ERR_INVALID_ARG;
+    return LPGEMM_OK;
+}
+
+lpgemm_status run_product(const MxArgs &g, int format, hipStream_t stream)
+{
+    (void)hipGetLastError();
+    switch (format) {
+    case OUT_F32: return launch_product<OUT_F32>(g, stream);
+    case OUT_BF16: return launch_product<OUT_BF16>(g, stream);
+    default: return launch_product<OUT_F16>(g, stream);
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+lpgemm_status lpgemm_mxfp4_quantize(const void *X, lpgemm_out_dtype x_dtype, int64_t ldx, uint8_t *codes,
+                                    uint8_t *scales, int64_t rows, int64_t K, hipStream_t stream)
+{
+    const int f = format_of(x_dtype);
+    const lpgemm_status st = check_values(X, codes, scales, f, rows, K);
+    if (st != LPGEMM_OK || rows == 0 || K == 0) return st;
+    if (ldx < (rows > 1 ? K : 0) || (rows > 1 && ldx > (INT64_MAX >> 4) / rows)) return LPGEMM_ERR_INVALID_ARG;
+    const int64_t units = ceil_div(K, kMxUnit);
+    const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(rows * units * 16, 256), 1 << 20);
+    uint32_t *c = reinterpret_cast<uint32_t *>(codes);
+    (void)hipGetLastError();
+    switch (f) {
+    case OUT_F32:
+        hipLaunchKernelGGL((mxfp4_quantize_kernel<OUT_F32>), dim3(blocks), dim3(256), 0, stream, X, ldx, c, scales, rows, K, units);
+        break;
+    case OUT_BF16:
+        hipLaunchKernelGGL((mxfp4_quantize_kernel<OUT_BF16>), dim3(blocks), dim3(256), 0, stream, X, ldx, c, scales, rows, K, units);
+        break;
+    default:
+        hipLaunchKernelGGL((mxfp4_quantize_kernel<OUT_F16>), dim3(blocks), dim3(256), 0, stream, X, ldx, c, scales, rows, K, units);
+    }
+    return launched();
+}
+
+lpgemm_status lpgemm_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, void *Y, lpgemm_out_dtype y_dtype,
+                                      int64_t rows, int64_t K, hipStream_t stream)
+{
+    const int f = format_of(y_dtype);
+    const lpgemm_status st = check_values(Y, codes, scales, f, rows, K);
+    if (st != LPGEMM_OK || rows == 0 || K == 0) return st;
+    const int64_t units = ceil_div(K, kMxUnit);
+    const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(rows * units * 16, 256), 1 << 20);
+    const uint32_t *c = reinterpret_cast<const uint32_t *>(codes);
+    (void)hipGetLastError();
+    switch (f) {
+    case OUT_F32:
+        hipLaunchKernelGGL((mxfp4_dequantize_kernel<OUT_F32>), dim3(blocks), dim3(256), 0, stream, c, scales, Y, rows, K, units);
+        break;
+    case OUT_BF16:
+        hipLaunchKernelGGL((mxfp4_dequantize_kernel<OUT_BF16>), dim3(blocks), dim3(256), 0, stream, c, scales, Y, rows, K, units);
+        break;
+    default:
+        hipLaunchKernelGGL((mxfp4_dequantize_kernel<OUT_F16>), dim3(blocks), dim3(256), 0, stream, c, scales, Y, rows, K, units);
+    }
+    return launched();
+}
+
+lpgemm_status lpgemm_mxfp4(const uint8_t *A, const uint8_t *SFA, const uint8_t *B, const uint8_t *SFB, void *D,
+                           lpgemm_out_dtype out_dtype, int64_t M, int64_t N, int64_t K, void *workspace,
+                           size_t workspace_bytes, hipStream_t stream)
+{
+    const int f = format_of(out_dtype);
+    const lpgemm_status st = check_product(A, SFA, B, SFB, D, f, M, M, N, K, 1);
+    if (st != LPGEMM_OK) return st;
+    if (workspace_bytes > 0 && (workspace == nullptr || !aligned(workspace, 256))) return LPGEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return LPGEMM_OK;
+    const MxArgs g{A, SFA, B, SFB, D, nullptr, nullptr, (int32_t)M, (int32_t)M, (int32_t)N, (int32_t)ceil_div(K, kMxUnit), 1};
+    return run_product(g, f, stream);
+}
+
+lpgemm_status lpgemm_mxfp4_workspace_size(int64_t M, int64_t N, int64_t K, int32_t cu_count, size_t *bytes)
+{
+    (void)cu_count;
+    if (bytes == nullptr || M < 0 || N < 0 || K < 0) return LPGEMM_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (K > LPGEMM_MXFP4_MAX_K || M > LPGEMM_MXFP4_MAX_ROWS || N > LPGEMM_MXFP4_MAX_ROWS) return LPGEMM_ERR_UNSUPPORTED;
+    return LPGEMM_OK;
+}
+
+lpgemm_status lpgemm_mxfp4_grouped(const uint8_t *A, const uint8_t *SFA, int64_t T, const int32_t *rows,
+                                   const uint8_t *B, const uint8_t *SFB, int64_t E, const int32_t *offsets, void *D,
+                                   lpgemm_out_dtype out_dtype, int64_t R, int64_t N, int64_t K, hipStream_t stream)
+{
+    const int f = format_of(out_dtype);
+    const lpgemm_status st = check_product(A, SFA, B, SFB, D, f, T, R, N, K, E);
+    if (st != LPGEMM_OK) return st;
+    if (rows == nullptr && T != R) return LPGEMM_ERR_INVALID_ARG;
+    if (E > LPGEMM_MXFP4_MAX_GROUPS) return LPGEMM_ERR_UNSUPPORTED;
+    const int64_t units = ceil_div(K, kMxUnit);
+    if (rows != nullptr && T * units * kMxUnitCodes > INT32_MAX) return LPGEMM_ERR_UNSUPPORTED;
+    if (R == 0 || N == 0 || E == 0) return LPGEMM_OK;
+    if (offsets == nullptr || !aligned(offsets, 4) || !aligned(rows, 4)) return LPGEMM_ERR_INVALID_ARG;
+    if (T == 0) {  // every row of D is of zeros; the kernels' dead reads of A need an address
+        A = B;
+        SFA = SFB;
+    }
+    const MxArgs g{A, SFA, B, SFB, D, offsets, rows, (int32_t)T, (int32_t)R, (int32_t)N, (int32_t)units, (int32_t)E};
+    return run_product(g, f, stream);
+}
+
+}  // extern "C"
