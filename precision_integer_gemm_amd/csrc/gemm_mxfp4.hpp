@@ -88,4 +88,380 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_simple_kernel(MxArgs g)
     }
 }
 
+// ---- tiled kernel ------------------------------------------------------------
+// 16 bytes (4 bytes) per lane from rsrc[voffset] into LDS at lds_base + 16 (4) lane;
+// offsets at or past the resource's size read zeros.
+__device__ __forceinline__ void mx_dma16(i32x4 rsrc, uint32_t voffset, uint32_t lds_base)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 : : "v"(voffset), "s"(rsrc), "s"(lds_base) : "memory", "m0");
+}
+__device__ __forceinline__ void mx_dma4(i32x4 rsrc, uint32_t voffset, uint32_t lds_base)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+                 : : "v"(voffset), "s"(rsrc), "s"(lds_base) : "memory", "m0");
+}
+
+typedef float mx_f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 mx_bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 mx_f16x2 __attribute__((ext_vector_type(2)));
+
+// Two binary32 values as two bf16 or fp16, nearest even, in one dword.
+template <int OUT>
+__device__ __forceinline__ uint32_t mx_pack2(float a, float b)
+{
+    const mx_f32x2 v = {a, b};
+    if (OUT == OUT_BF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, mx_bf16x2));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, mx_f16x2));
+}
+
+// A workgroup of four waves (2 x 2) computes tiles of 64 FM x 64 FN, FM = 1 ..
+// FN chosen tile by tile from its group's rows, so a group wastes less than 64
+// rows whatever its size; a wave holds FM x FN blocks of 32 x 32.
+//
+// A stage is two units (256 k) of every row: 128 code bytes, one cache line,
+// and 8 scale bytes.  Lane half h of a wave takes unit h of the stage, MFMA
+// step s its block s, so one dword of scales serves a lane's four steps, the
+// MFMA picking byte s.  In LDS a row's eight 16-byte chunks are permuted by
+// c -> c ^ (row / 2) % 8: both the copies (8 rows of 128 bytes each) and the
+// fragment reads (16 rows of one chunk) touch all banks once.
+template <int FN>
+struct MxTile {
+    static constexpr int BN = 64 * FN;
+    static constexpr int NB = 2 * FN;                       // a wave's code copies of B per stage
+    static constexpr int NSB = FN >= 4 ? FN / 4 * 2 : 1;    // and its scale copies (32 rows each)
+    static constexpr int nsa(int fm) { return fm > 2 ? 2 : 1; }
+    static constexpr int per(int fm) { return NB + 2 * fm + NSB + nsa(fm); }
+    static constexpr int stage(int fm) { return (BN + 64 * fm) * 128 + (NSB + nsa(fm)) * 1024; }
+    // one workgroup per compute unit for the large tile, two for the others
+    static constexpr int kBudget = FN == 4 ? 158 * 1024 : 76 * 1024;
+    static constexpr int stages(int fm) { return kBudget / stage(fm) > 4 ? 4 : kBudget / stage(fm); }
+    static constexpr int ring(int fm) { return fm == 0 ? 0 : stages(fm) * stage(fm) > ring(fm - 1) ? stages(fm) * stage(fm) : ring(fm - 1); }
+    static constexpr int kRing = ring(FN);
+    static_assert(stages(FN) >= 2, "two stages at least");
+};
+
+template <int FN, int OUT>
+__global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(MxArgs g, int tiles_n, int xcds)
+{
+    using T = MxTile<FN>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    int32_t *cum = reinterpret_cast<int32_t *>(smem + T::kRing);  // [E + 1]: row tiles before group e
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int r32 = lane & 31, h = lane >> 5;
+    const int U = g.U, ktiles = (U + 1) / 2;
+    const uint32_t ldc = (uint32_t)U * kMxUnitCodes, lds_ = (uint32_t)U * kMxUnitScales;
+    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(smem);
+
+    // Row tiles of every group, summed: thread t takes groups t P .. t P + P - 1.
+    int total_rt;
+    if (g.offsets == nullptr) {
+        total_rt = (g.R + 64 * FN - 1) / (64 * FN);
+    } else {
+        int32_t *part = cum + g.E + 1;
+        const int P = (g.E + 255) / 256;
+        int sum = 0;
+        for (int i = 0; i < P; ++i) {
+            const int e = tid * P + i;
+            int b = 0, f = 0;
+            if (e < g.E) mx_group(g, e, b, f);
+            sum += (f - b + 64 * FN - 1) / (64 * FN);
+        }
+        int run = sum;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int o = __shfl_up(run, d);
+            if (lane >= d) run += o;
+        }
+        if (lane == 63) part[wave] = run;
+        __syncthreads();
+        int before = run - sum;
+        for (int w = 0; w < wave; ++w) before += part[w];
+        for (int i = 0; i < P; ++i) {
+            const int e = tid * P + i;
+            if (e >= g.E) break;
+            int b, f;
+            mx_group(g, e, b, f);
+            cum[e] = before;
+            before += (f - b + 64 * FN - 1) / (64 * FN);
+            if (e == g.E - 1) cum[g.E] = before;
+        }
+        __syncthreads();
+        total_rt = __builtin_amdgcn_readfirstlane(cum[g.E]);
+    }
+    const int total = total_rt * tiles_n;
+    const int whole = total - total % xcds;
+
+    // The current tile: group e, rows [m0, m1) of D, columns from n0, height 64 fm.
+    int e = 0, m0 = 0, m1 = 0, n0 = 0, fm = 0;
+    auto find = [&](int v) __attribute__((always_inline)) {
+        // XCD-contiguous: workgroups v, v + 8, .. share an L2 and take neighbouring tiles
+        const int id = v < whole ? (v % xcds) * (whole / xcds) + v / xcds : v;
+        int begin = 0, end = g.R, first = 0;
+        e = 0;
+        if (g.offsets != nullptr) {
+            const int rt = id / tiles_n;
+            int n = 0;
+            for (int i = 0; i < g.E; i += 64)
+                n += (int)__popcll(__ballot(i + lane < g.E && cum[i + lane] <= rt));
+            e = __builtin_amdgcn_readfirstlane(n - 1);
+            first = __builtin_amdgcn_readfirstlane(cum[e]);
+            mx_group(g, e, begin, end);
+        }
+        begin = __builtin_amdgcn_readfirstlane(begin);
+        end = __builtin_amdgcn_readfirstlane(end);
+        const int blocks = (end - begin + 63) / 64, c = (blocks + FN - 1) / FN;  // of 64 rows; tiles
+        // bands of four row tiles, the band's tiles of one column together
+        const int in_group = id - first * tiles_n;
+        const int band = in_group / (4 * tiles_n), high = min(4, c - 4 * band);
+        const int in_band = in_group - band * 4 * tiles_n;
+        const int j = 4 * band + in_band % high;
+        n0 = in_band / high * T::BN;
+        // the group's blocks, shared out evenly
+        fm = blocks / c + (j < blocks % c ? 1 : 0);
+        m0 = begin + 64 * (j * (blocks / c) + min(j, blocks % c));
+        m1 = min(end, m0 + 64 * fm);
+    };
+
+    // Source offsets of this lane in each copy of a stage.
+    i32x4 rsrc_a, rsrc_sa, rsrc_b, rsrc_sb;
+    uint32_t a_off[2 * FN], sa_off[2], b_off[T::NB], sb_off[T::NSB];
+    const int c8 = lane & 7;
+    // chunk of the row's 128 bytes that goes to position c8 of row 8 p + lane / 8
+    auto chunk = [&](int p) { return c8 ^ ((4 * p + (lane >> 4)) & 7); };
+#pragma unroll
+    for (int i = 0; i < T::NB; ++i) {
+        const int p = wave * T::NB + i;
+        b_off[i] = (uint32_t)(8 * p + (lane >> 3)) * ldc + 16u * (uint32_t)chunk(p);
+    }
+#pragma unroll
+    for (int i = 0; i < T::NSB; ++i) {
+        const int blk = wave * T::NSB + i;
+        sb_off[i] = 32 * blk < T::BN ? (uint32_t)(32 * blk + r32) * lds_ + 4u * (uint32_t)h : kOutOfRange;
+    }
+    auto place = [&]() __attribute__((always_inline)) {  // resources and A's offsets of the current tile
+        const int64_t brow = (int64_t)e * g.N + n0;
+        const uint32_t nrows = (uint32_t)min(T::BN, g.N - n0);
+        rsrc_b = make_rsrc(g.B + brow * ldc, nrows * ldc);
+        rsrc_sb = make_rsrc(g.SFB + brow * lds_, nrows * lds_);
+        if (g.rows == nullptr) {
+            rsrc_a = make_rsrc(g.A + (int64_t)m0 * ldc, (uint32_t)(m1 - m0) * ldc);
+            rsrc_sa = make_rsrc(g.SFA + (int64_t)m0 * lds_, (uint32_t)(m1 - m0) * lds_);
+        } else {
+            rsrc_a = make_rsrc(g.A, (uint32_t)g.T * ldc);
+            rsrc_sa = make_rsrc(g.SFA, (uint32_t)g.T * lds_);
+        }
+        auto row_offset = [&](int r, uint32_t ld) __attribute__((always_inline)) -> uint32_t {  // of tile row r
+            if (g.rows == nullptr) return (uint32_t)r * ld;
+            const int at = m0 + r < m1 ? g.rows[m0 + r] : -1;
+            return at >= 0 && at < g.T ? (uint32_t)at * ld : kOutOfRange;
+        };
+#pragma unroll
+        for (int i = 0; i < 2 * FN; ++i) {
+            const int p = wave * 2 * fm + i;
+            if (i < 2 * fm) a_off[i] = row_offset(8 * p + (lane >> 3), ldc) + 16u * (uint32_t)chunk(p);
+        }
+        const int n = fm > 2 ? 2 : 1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int blk = wave * n + i;
+            sa_off[i] = blk < 2 * fm ? row_offset(32 * blk + r32, lds_) + 4u * (uint32_t)h : kOutOfRange;
+        }
+    };
+
+    // Copy j of stage kt's copies into the slot at `base`, for tiles of height
+    // 64 f.  Units past the row read zeros (zero codes: the scale beside them
+    // does not matter).
+    auto issue = [&](int j, int f, int kt, uint32_t base) __attribute__((always_inline)) {
+        const uint32_t a0 = base + T::BN * 128, sb0 = a0 + (uint32_t)(64 * f) * 128, sa0 = sb0 + T::NSB * 1024;
+        const uint32_t koff = (uint32_t)kt * 128u, soff = (uint32_t)kt * 8u;
+        if (j < T::NB) {
+            const int p = wave * T::NB + j;
+            const bool in = 2 * kt + (chunk(p) >> 2) < U;
+            mx_dma16(rsrc_b, in ? b_off[j] + koff : kOutOfRange, base + (uint32_t)p * 1024u);
+        } else if (j < T::NB + T::NSB) {
+            const int i = j - T::NB;
+            mx_dma4(rsrc_sb, 2 * kt + h < U ? sb_off[i] + soff : kOutOfRange, sb0 + (uint32_t)(wave * T::NSB + i) * 256u);
+        } else if (j < T::NB + T::NSB + 2 * f) {
+            const int i = j - T::NB - T::NSB, p = wave * 2 * f + i;
+            const bool in = 2 * kt + (chunk(p) >> 2) < U;
+            mx_dma16(rsrc_a, in ? a_off[i] + koff : kOutOfRange, a0 + (uint32_t)p * 1024u);
+        } else {
+            const int i = j - T::NB - T::NSB - 2 * f, n = T::nsa(f);
+            mx_dma4(rsrc_sa, 2 * kt + h < U ? sa_off[i] + soff : kOutOfRange, sa0 + (uint32_t)(wave * n + i) * 256u);
+        }
+    };
+    // dispatch on the height; bodies see it as a constant
+    auto with_height = [&](auto body) __attribute__((always_inline)) {
+        if (FN >= 4 && fm == 4) body(std::integral_constant<int, FN >= 4 ? 4 : 1>{});
+        else if (FN >= 4 && fm == 3) body(std::integral_constant<int, FN >= 4 ? 3 : 1>{});
+        else if (FN >= 2 && fm == 2) body(std::integral_constant<int, FN >= 2 ? 2 : 1>{});
+        else body(std::integral_constant<int, 1>{});
+    };
+    auto prologue = [&]() __attribute__((always_inline)) {
+        with_height([&](auto height) __attribute__((always_inline)) {
+            constexpr int FM = decltype(height)::value;
+#pragma nounroll
+            for (int st = 0; st < T::stages(FM); ++st)
+#pragma unroll
+                for (int j = 0; j < T::per(FM); ++j) issue(j, FM, st, lds0 + (uint32_t)(st * T::stage(FM)));
+        });
+    };
+
+    f32x16 acc[FN][FN];  // [n block][m block]
+    int pending = 0;     // store instructions of the previous tile, at least
+    auto contract = [&](auto height) __attribute__((always_inline)) {
+        constexpr int FM = decltype(height)::value;
+        constexpr int ST = T::stages(FM), PER = T::per(FM), STAGE = T::stage(FM);
+        constexpr uint32_t kA = T::BN * 128, kSB = kA + 64 * FM * 128, kSA = kSB + T::NSB * 1024;
+        constexpr int kBlocks = FM * FN, kReads = FM + FN;
+        if (pending >= 32)
+            wait_vmcnt<(ST - 1) * PER + 32>();
+        else if (pending >= 16)
+            wait_vmcnt<(ST - 1) * PER + 16>();
+        else
+            wait_vmcnt<(ST - 1) * PER>();
+        lds_barrier();
+
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j) acc[i][j] = f32x16{};
+
+        i32x4 fb[2][FN], fa[2][FM];
+        uint32_t sb[FN], sa[FM], sb_next[FN], sa_next[FM];
+        const int swz = (r32 >> 1) & 7;
+        // fragment i of step s: B's blocks, then A's
+        auto read = [&](int s, int i, const uint8_t *base) __attribute__((always_inline)) {
+            const uint32_t at = (uint32_t)r32 * 128u + 16u * (uint32_t)((4 * h + s) ^ swz);
+            if (i < FN)
+                fb[s & 1][i] = load16(base + (wn * FN + i) * 4096 + at);
+            else
+                fa[s & 1][i - FN] = load16(base + kA + (wm * FM + i - FN) * 4096 + at);
+        };
+        auto read_scale = [&](int i, const uint8_t *base) __attribute__((always_inline)) {
+            if (i < FN)
+                sb_next[i] = *reinterpret_cast<const uint32_t *>(base + kSB + (wn * FN + i) * 256 + 4 * lane);
+            else
+                sa_next[i - FN] = *reinterpret_cast<const uint32_t *>(base + kSA + (wm * FM + i - FN) * 256 + 4 * lane);
+        };
+        auto take_scales = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i) sb[i] = sb_next[i];
+#pragma unroll
+            for (int i = 0; i < FM; ++i) sa[i] = sa_next[i];
+        };
+#pragma unroll
+        for (int i = 0; i < kReads; ++i) {
+            read_scale(i, smem);
+            read(0, i, smem);
+        }
+        take_scales();
+        // Step S: the next step's reads go out after the first MFMAs, the
+        // copies that refill the stage's slot between all of the last step's.
+        constexpr int kPer = (kReads + kBlocks - 1) / kBlocks;
+        auto step = [&](auto index, const uint8_t *next, bool reads, bool refill, int kt, uint32_t slot_base) __attribute__((always_inline)) {
+            constexpr int S = decltype(index)::value;
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const int fn = b / FM, f = b % FM;
+                acc[fn][f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(fb[S & 1][fn]), mx_operand(fa[S & 1][f]),
+                                                                             acc[fn][f], kMxFormat, kMxFormat, S, sb[fn], S, sa[f]);
+#pragma unroll
+                for (int i = 0; i < kReads; ++i)
+                    if (reads && i / kPer == b) {
+                        read((S + 1) & 3, i, next);
+                        if (S == 3) read_scale(i, next);
+                    }
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    if (refill && j >= b * PER / kBlocks && j < (b + 1) * PER / kBlocks) issue(j, FM, kt + ST, slot_base);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        using i0 = std::integral_constant<int, 0>;
+        using i1 = std::integral_constant<int, 1>;
+        using i2 = std::integral_constant<int, 2>;
+        using i3 = std::integral_constant<int, 3>;
+        int slot = 0;
+        for (int kt = 0; kt + 1 < ktiles; ++kt) {
+            const uint8_t *base = smem + slot * STAGE;
+            const uint32_t lbase = lds0 + (uint32_t)(slot * STAGE);
+            slot = slot + 1 == ST ? 0 : slot + 1;
+            const uint8_t *next = smem + slot * STAGE;
+            step(i0{}, base, true, false, kt, 0);
+            step(i1{}, base, true, false, kt, 0);
+            step(i2{}, base, true, false, kt, 0);
+            wait_vmcnt<(ST - 2) * PER>();
+            lds_barrier();
+            step(i3{}, next, true, true, kt, lbase);
+            take_scales();
+        }
+        const uint8_t *base = smem + slot * STAGE;
+        step(i0{}, base, true, false, 0, 0);
+        step(i1{}, base, true, false, 0, 0);
+        step(i2{}, base, true, false, 0, 0);
+        step(i3{}, base, false, false, 0, 0);
+        wait_vmcnt<0>();  // copies past the last stage
+    };
+
+    int v = blockIdx.x;
+    if (v >= total) return;
+    find(v);
+    place();
+    prologue();
+    for (;;) {
+        with_height(contract);
+
+        const int tm0 = m0, tm1 = m1, tn0 = n0, tfm = fm;
+        v += (int)gridDim.x;
+        lds_barrier();  // every wave is done with the ring
+        if (v < total) {
+            find(v);
+            place();
+            prologue();
+        }
+        // Stores: bf16 and fp16 exchange halves so that a lane has eight
+        // neighbouring columns of one row, 16 bytes.
+        const bool wide = OUT != OUT_F32 && g.N % 8 == 0;
+#pragma unroll
+        for (int f = 0; f < FN; ++f) {
+            if (f >= tfm) break;
+            const int m = tm0 + (wm * tfm + f) * 32 + r32;
+#pragma unroll
+            for (int fn = 0; fn < FN; ++fn) {
+                const int nb = tn0 + (wn * FN + fn) * 32;
+                const f32x16 c = acc[fn][f];
+                if (wide) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint32_t x0 = mx_pack2<OUT>(c[8 * q + 0], c[8 * q + 1]), x1 = mx_pack2<OUT>(c[8 * q + 2], c[8 * q + 3]);
+                        const uint32_t y0 = mx_pack2<OUT>(c[8 * q + 4], c[8 * q + 5]), y1 = mx_pack2<OUT>(c[8 * q + 6], c[8 * q + 7]);
+                        const auto s0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
+                        const auto s1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
+                        const int n = nb + 16 * q + 8 * h;
+                        if (m < tm1 && n < g.N)
+                            *reinterpret_cast<i32x4 *>(static_cast<uint16_t *>(g.D) + (int64_t)m * g.N + n) =
+                                i32x4{(int32_t)s0[0], (int32_t)s1[0], (int32_t)s0[1], (int32_t)s1[1]};
+                    }
+                } else if (m < tm1) {
+                    Epilogue epi{g.D, nullptr, nullptr};
+#pragma unroll
+                    for (int rg = 0; rg < 4; ++rg) {
+                        const float x[4] = {c[4 * rg], c[4 * rg + 1], c[4 * rg + 2], c[4 * rg + 3]};
+                        store_row4f<OUT>(epi, m, g.N, nb + 8 * rg + 4 * h, x);
+                    }
+                }
+            }
+        }
+        if (v >= total) break;
+        // whole tiles issue one store per 16 bytes and lane; others count as none
+        const bool full = tm0 + 64 * tfm <= tm1 && tn0 + T::BN <= g.N;
+        pending = full && (OUT == OUT_F32 ? g.N % 4 == 0 : wide) ? tfm * FN * (OUT == OUT_F32 ? 4 : 2) : 0;
+    }
+}
+
 }  // namespace lpgemm

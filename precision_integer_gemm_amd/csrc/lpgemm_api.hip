@@ -10,6 +10,7 @@
 #include "gemm_skinny.hpp"
 #include "gemm_pipelined.hpp"
 #include "gemm_fp6.hpp"
+#include "host_common.hpp"
 
 using namespace lpgemm;
 
@@ -37,6 +38,13 @@ int device_cu_count()
     });
     return cus[dev];
 }
+
+}  // namespace
+
+int lpgemm::forced_kernel() { return t_override; }
+int lpgemm::compute_units() { return device_cu_count(); }
+
+namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

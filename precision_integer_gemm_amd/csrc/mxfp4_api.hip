@@ -3,8 +3,10 @@
 #include "lpgemm.h"
 
 #include <algorithm>
+#include <mutex>
 
 #include "gemm_mxfp4.hpp"
+#include "host_common.hpp"
 #include "mxfp4_quantize.hpp"
 
 using namespace lpgemm;
@@ -41,12 +43,65 @@ lpgemm_status check_values(const void *x, const void *codes, const void *scales,
     return LPGEMM_OK;
 }
 
+constexpr int kMaxDevices = 64;
+constexpr int kXcds = 8;  // MI355X: 8 XCDs, workgroup ids dealt round robin over them
+
+// Dynamic LDS above 64 KB has to be asked for, once per kernel and device.
+template <typename Kernel>
+lpgemm_status allow_lds(Kernel kernel, int bytes, std::once_flag *once, hipError_t *err)
+{
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return LPGEMM_ERR_HIP;
+    std::call_once(once[dev], [&] {
+        err[dev] = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    });
+    return err[dev] == hipSuccess ? LPGEMM_OK : LPGEMM_ERR_HIP;
+}
+
+template <int FN, int OUT>
+lpgemm_status launch_tiled(const MxArgs &g, hipStream_t stream)
+{
+    using T = MxTile<FN>;
+    static std::once_flag once[kMaxDevices];
+    static hipError_t err[kMaxDevices];
+    const auto kernel = &gemm_mxfp4_tiled_kernel<FN, OUT>;
+    constexpr int kLds = T::kRing + 4 * (LPGEMM_MXFP4_MAX_GROUPS + 1 + 4);
+    const lpgemm_status st = allow_lds(kernel, kLds, once, err);
+    if (st != LPGEMM_OK) return st;
+    const int tiles_n = (int)ceil_div(g.N, 64 * FN);
+    // at most one ragged row tile a group more than the rows fill
+    const int64_t most = (ceil_div(g.R, 64 * FN) + (g.offsets ? std::min(g.E, g.R) : 0)) * tiles_n;
+    const unsigned blocks = (unsigned)std::min<int64_t>(most, (int64_t)compute_units() * (FN == 4 ? 1 : 2));
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), kLds, stream, g, tiles_n, kXcds);
+    return launched();
+}
+
 template <int OUT>
-lpgemm_status launch_product(const MxArgs &g, hipStream_t stream)
+lpgemm_status launch_simple(const MxArgs &g, hipStream_t stream)
 {
     const dim3 grid((unsigned)ceil_div(g.N, 128), (unsigned)std::min<int64_t>(ceil_div(g.R, 32), 65535), (unsigned)g.E);
     hipLaunchKernelGGL((gemm_mxfp4_simple_kernel<OUT>), grid, dim3(256), 0, stream, g);
     return launched();
+}
+
+template <int OUT>
+lpgemm_status launch_product(const MxArgs &g, hipStream_t stream)
+{
+    const int64_t cu = compute_units();
+    auto tiles = [&](int64_t edge) { return (ceil_div(g.R, edge) + (g.offsets ? g.E / 2 : 0)) * ceil_div(g.N, edge); };
+    int tile = 4 * tiles(256) >= 3 * cu ? 256 : tiles(128) >= cu ? 128 : 64;
+    switch (forced_kernel()) {
+    case LPGEMM_KERNEL_AUTO:
+    case LPGEMM_KERNEL_TILED: break;
+    case LPGEMM_KERNEL_GENERAL: return launch_simple<OUT>(g, stream);
+    case LPGEMM_KERNEL_TILED_64: tile = 64; break;
+    case LPGEMM_KERNEL_TILED_128: tile = 128; break;
+    case LPGEMM_KERNEL_TILED_256: tile = 256; break;
+    default: return LPGEMM_ERR_UNSUPPORTED;
+    }
+    // 32-bit row tile counts and offsets of a tile's rows
+    if (ceil_div(g.R, tile) + g.E > INT32_MAX / ceil_div(g.N, tile)) return LPGEMM_ERR_UNSUPPORTED;
+    return tile == 256 ? launch_tiled<4, OUT>(g, stream) : tile == 128 ? launch_tiled<2, OUT>(g, stream) : launch_tiled<1, OUT>(g, stream);
 }
 
 // Sizes and pointers that both products share; R rows of D.
