@@ -468,6 +468,31 @@ def lpgemm_unpack_int4(packed, *, out=None, stream=None):
 
 
 # ---- microscaled 4-bit floating point ------------------------------------------
+# These calls take a few microseconds on the device for a token's work, so what
+# the host does before a launch is kept short.
+_mx = None  # torch, the library and the result types' codes, once both are loaded
+
+
+def _mx_torch():
+    global _mx
+    if _mx is None:
+        torch = _torch()
+        _mx = (torch, lib(), {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16, torch.float16: OUT_F16})
+    return _mx[0]
+
+
+def _mx_launch(function, index, stream, *args):
+    """Calls a library function on the tensors' device: on `stream`, or that device's current one."""
+    torch = _mx[0]
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _mx_launch(function, index, stream, *args)
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    status = function(*args, handle)
+    if status != OK:
+        _raise(status, function.__name__)
+
+
 def _units(K: int) -> int:
     return -(-K // MXFP4_UNIT)
 
@@ -489,8 +514,23 @@ def _check_on(t, name: str, dtypes, dim: int, device=None):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _mx_units(codes, scales, name: str, dim: int, device=None):
+    """Units per row of an mxfp4 operand.  One expression passes what is right;
+    what is not goes through the checks that say what is wrong."""
+    u8 = _mx_torch().uint8
+    try:
+        c, s = codes.shape, scales.shape
+        units = c[-1] // MXFP4_UNIT_CODES
+        if (codes.dtype is u8 and scales.dtype is u8 and codes.is_cuda and len(c) == dim and c[:-1] == s[:-1]
+                and units * MXFP4_UNIT_CODES == c[-1] and units * MXFP4_UNIT_SCALES == s[-1] and codes.is_contiguous()
+                and scales.is_contiguous() and scales.device == (device or codes.device) and (device is None or codes.device == device)):
+            return units
+    except (AttributeError, IndexError):
+        pass
+    return _check_mx(codes, scales, name, dim, device)
+
+
 def _check_mx(codes, scales, name: str, dim: int, device=None):
-    """Units per row of an mxfp4 operand."""
     torch = _torch()
     _check_on(codes, name, (torch.uint8,), dim, device)
     _check_on(scales, f"scales of {name}", (torch.uint8,), dim, codes.device)
@@ -502,14 +542,17 @@ def _check_mx(codes, scales, name: str, dim: int, device=None):
 
 
 def _mx_out(out, dtype, M, N, device):
-    torch = _torch()
+    torch, _, codes = _mx
     if out is None:
         dtype = dtype or torch.bfloat16
-        return torch.empty((M, N), dtype=dtype, device=device), _out_code(dtype)
-    _check_on(out, "out", (dtype or out.dtype,), 2, device)
+        code = codes.get(dtype)
+        if code is None:
+            raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+        return torch.empty((M, N), dtype=dtype, device=device), code
+    _check_on(out, "out", (dtype,) if dtype else tuple(codes), 2, device)
     if tuple(out.shape) != (M, N):
         raise ValueError(f"out must have shape ({M}, {N}), got {tuple(out.shape)}")
-    return out, _out_code(out.dtype)
+    return out, codes[out.dtype]
 
 
 def lpgemm_mxfp4_quantize(x, *, codes=None, scales=None, stream=None):
@@ -517,42 +560,51 @@ def lpgemm_mxfp4_quantize(x, *, codes=None, scales=None, stream=None):
     [rows, 64 U], scales uint8 [rows, 4 U]) with U = ceil(K / 128): e2m1 codes
     and one e8m0 scale byte per 32 values.  Rows of x may be strided (its last
     dimension is dense)."""
-    torch = _torch()
+    torch = _mx_torch()
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
-    code = _out_code(x.dtype)
+    code = _mx[2].get(x.dtype)
+    if code is None:
+        raise TypeError(f"x must be float32, bfloat16 or float16, got {x.dtype}")
     if x.dim() != 2:
         raise ValueError(f"x must be 2-D, got shape {tuple(x.shape)}")
     if not x.is_cuda:
         raise ValueError(f"x must be on a GPU device, got {x.device}")
     rows, K = x.shape
-    ldx = x.stride(0)
-    if (K > 1 and x.stride(1) != 1) or (rows > 1 and ldx < K):
+    ldx, step = x.stride()
+    if (K > 1 and step != 1) or (rows > 1 and ldx < K):
         raise ValueError(f"x must be dense along its last dimension, its rows apart: strides {x.stride()}")
     U = _units(K)
-    for name, t, n in (("codes", codes, MXFP4_UNIT_CODES * U), ("scales", scales, MXFP4_UNIT_SCALES * U)):
-        if t is not None:
-            _check_on(t, name, (torch.uint8,), 2, x.device)
-            if tuple(t.shape) != (rows, n):
-                raise ValueError(f"{name} must have shape ({rows}, {n}), got {tuple(t.shape)}")
+    device = x.device
     if codes is None:
-        codes = torch.empty((rows, MXFP4_UNIT_CODES * U), dtype=torch.uint8, device=x.device)
+        codes = torch.empty((rows, MXFP4_UNIT_CODES * U), dtype=torch.uint8, device=device)
+    else:
+        _check_shape(codes, "codes", (rows, MXFP4_UNIT_CODES * U), device)
     if scales is None:
-        scales = torch.empty((rows, MXFP4_UNIT_SCALES * U), dtype=torch.uint8, device=x.device)
-    _raise(lib().lpgemm_mxfp4_quantize(x.data_ptr(), code, ldx, codes.data_ptr(), scales.data_ptr(), rows, K,
-                                       _stream_handle(stream)), "lpgemm_mxfp4_quantize")
+        scales = torch.empty((rows, MXFP4_UNIT_SCALES * U), dtype=torch.uint8, device=device)
+    else:
+        _check_shape(scales, "scales", (rows, MXFP4_UNIT_SCALES * U), device)
+    _mx_launch(_mx[1].lpgemm_mxfp4_quantize, device.index, stream, x.data_ptr(), code, ldx, codes.data_ptr(),
+               scales.data_ptr(), rows, K)
     return codes, scales
+
+
+def _check_shape(t, name: str, shape, device):
+    _check_on(t, name, (_torch().uint8,), 2, device)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
 
 def lpgemm_mxfp4_dequantize(codes, scales, K, *, dtype=None, out=None, stream=None):
     """The values [rows, K] that mxfp4 codes and scales stand for (bfloat16 by
     default; exact in float32 and bfloat16)."""
-    units = _check_mx(codes, scales, "codes", 2)
+    units = _mx_units(codes, scales, "codes", 2)
     if K < 0 or _units(K) != units:
         raise ValueError(f"K={K} does not fit {units} units of {MXFP4_UNIT} values")
-    out, code = _mx_out(out, dtype, codes.shape[0], K, codes.device)
-    _raise(lib().lpgemm_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), out.data_ptr(), code, codes.shape[0], K,
-                                         _stream_handle(stream)), "lpgemm_mxfp4_dequantize")
+    device, rows = codes.device, codes.shape[0]
+    out, code = _mx_out(out, dtype, rows, K, device)
+    _mx_launch(_mx[1].lpgemm_mxfp4_dequantize, device.index, stream, codes.data_ptr(), scales.data_ptr(), out.data_ptr(),
+               code, rows, K)
     return out
 
 
@@ -567,17 +619,18 @@ def lpgemm_mxfp4(A, SFA, B, SFB, *, dtype=None, out=None, workspace="auto", stre
     """D[M,N] = A . B^T of mxfp4 operands (codes [M, 64 U] and [N, 64 U], scales
     [M, 4 U] and [N, 4 U]) with fp32 accumulation, as bfloat16 (default),
     float16 or float32; workspace as for lpgemm_int4_int4."""
-    units = _check_mx(A, SFA, "A", 2)
-    if _check_mx(B, SFB, "B", 2, A.device) != units:
+    units = _mx_units(A, SFA, "A", 2)
+    device = A.device
+    if _mx_units(B, SFB, "B", 2, device) != units:
         raise ValueError(f"K mismatch: A has {A.shape[1]} bytes per row, B {B.shape[1]}")
     M, N, K = A.shape[0], B.shape[0], MXFP4_UNIT * units
-    D, code = _mx_out(out, dtype, M, N, A.device)
+    D, code = _mx_out(out, dtype, M, N, device)
     if isinstance(workspace, str) and workspace == "auto":
         n = lpgemm_mxfp4_workspace_size(M, N, K)
-        workspace = _torch().empty(n, dtype=_torch().uint8, device=A.device) if n else None
-    ws, nws, _keep = _workspace(workspace, None, M, N, K, True, A.device)
-    _raise(lib().lpgemm_mxfp4(A.data_ptr(), SFA.data_ptr(), B.data_ptr(), SFB.data_ptr(), D.data_ptr(), code, M, N, K,
-                              ws, nws, _stream_handle(stream)), "lpgemm_mxfp4")
+        workspace = _mx[0].empty(n, dtype=_mx[0].uint8, device=device) if n else None
+    ws, nws, _keep = _workspace(workspace, None, M, N, K, True, device)
+    _mx_launch(_mx[1].lpgemm_mxfp4, device.index, stream, A.data_ptr(), SFA.data_ptr(), B.data_ptr(), SFB.data_ptr(),
+               D.data_ptr(), code, M, N, K, ws, nws)
     return D
 
 
@@ -586,20 +639,21 @@ def lpgemm_mxfp4_grouped(A, SFA, B, SFB, offsets, *, rows=None, dtype=None, out=
     offsets[e] <= i < offsets[e + 1], is row rows[i] of A times B[e]^T (rows
     None: row i; an index outside A's rows stands for zeros).  A codes [T, 64 U],
     B codes [E, N, 64 U], offsets int32 [E + 1] and rows int32 on the device."""
-    torch = _torch()
-    units = _check_mx(A, SFA, "A", 2)
-    if _check_mx(B, SFB, "B", 3, A.device) != units:
+    units = _mx_units(A, SFA, "A", 2)
+    device = A.device
+    if _mx_units(B, SFB, "B", 3, device) != units:
         raise ValueError(f"K mismatch: A has {A.shape[1]} bytes per row, B {B.shape[2]}")
     E, N = B.shape[0], B.shape[1]
-    _check_on(offsets, "offsets", (torch.int32,), 1, A.device)
+    int32 = (_mx[0].int32,)
+    _check_on(offsets, "offsets", int32, 1, device)
     if offsets.shape[0] != E + 1:
         raise ValueError(f"offsets must have {E + 1} entries for {E} groups, got {offsets.shape[0]}")
     T = R = A.shape[0]
+    index = None
     if rows is not None:
-        _check_on(rows, "rows", (torch.int32,), 1, A.device)
-        R = rows.shape[0]
-    D, code = _mx_out(out, dtype, R, N, A.device)
-    _raise(lib().lpgemm_mxfp4_grouped(A.data_ptr(), SFA.data_ptr(), T, rows.data_ptr() if rows is not None else None,
-                                      B.data_ptr(), SFB.data_ptr(), E, offsets.data_ptr(), D.data_ptr(), code, R, N,
-                                      MXFP4_UNIT * units, _stream_handle(stream)), "lpgemm_mxfp4_grouped")
+        _check_on(rows, "rows", int32, 1, device)
+        R, index = rows.shape[0], rows.data_ptr()
+    D, code = _mx_out(out, dtype, R, N, device)
+    _mx_launch(_mx[1].lpgemm_mxfp4_grouped, device.index, stream, A.data_ptr(), SFA.data_ptr(), T, index, B.data_ptr(),
+               SFB.data_ptr(), E, offsets.data_ptr(), D.data_ptr(), code, R, N, MXFP4_UNIT * units)
     return D

@@ -102,9 +102,6 @@ __device__ __forceinline__ void mx_dma4(i32x4 rsrc, uint32_t voffset, uint32_t l
                  : : "v"(voffset), "s"(rsrc), "s"(lds_base) : "memory", "m0");
 }
 
-typedef float mx_f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 mx_bf16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 mx_f16x2 __attribute__((ext_vector_type(2)));
 
 // Two binary32 values as two bf16 or fp16, nearest even, in one dword.
 template <int OUT>

@@ -43,6 +43,36 @@ lpgemm_status check_values(const void *x, const void *codes, const void *scales,
     return LPGEMM_OK;
 }
 
+// Items of eight values; four a thread where that leaves four workgroups a
+// compute unit, else one.
+constexpr int64_t kManyItems = 4 * 256 * 4 * 256;
+
+template <int IN>
+lpgemm_status launch_quantize(const void *x, int64_t ldx, uint8_t *codes, uint8_t *scales, int64_t rows, int64_t K, hipStream_t stream)
+{
+    const int64_t items = ceil_div(K, kMxUnit) * (kMxUnit / 8), total = rows * items;
+    const bool many = total >= kManyItems;
+    const int64_t blocks = ceil_div(total, many ? 1024 : 256);
+    if (blocks > INT32_MAX) return LPGEMM_ERR_UNSUPPORTED;
+    const auto kernel = many ? &mxfp4_quantize_kernel<IN, 4> : &mxfp4_quantize_kernel<IN, 1>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, stream, x, ldx, reinterpret_cast<uint32_t *>(codes), scales, rows,
+                       (int32_t)K, (uint32_t)items);
+    return launched();
+}
+
+template <int OUT>
+lpgemm_status launch_dequantize(const uint8_t *codes, const uint8_t *scales, void *y, int64_t rows, int64_t K, hipStream_t stream)
+{
+    const int64_t items = ceil_div(K, kMxUnit) * (kMxUnit / 8), total = rows * items;
+    const bool many = total >= kManyItems;
+    const int64_t blocks = ceil_div(total, many ? 1024 : 256);
+    if (blocks > INT32_MAX) return LPGEMM_ERR_UNSUPPORTED;
+    const auto kernel = many ? &mxfp4_dequantize_kernel<OUT, 4> : &mxfp4_dequantize_kernel<OUT, 1>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, stream, reinterpret_cast<const uint32_t *>(codes), scales, y, rows,
+                       (int32_t)K, (uint32_t)items);
+    return launched();
+}
+
 constexpr int kMaxDevices = 64;
 constexpr int kXcds = 8;  // MI355X: 8 XCDs, workgroup ids dealt round robin over them
 
@@ -140,21 +170,12 @@ lpgemm_status lpgemm_mxfp4_quantize(const void *X, lpgemm_out_dtype x_dtype, int
     const lpgemm_status st = check_values(X, codes, scales, f, rows, K);
     if (st != LPGEMM_OK || rows == 0 || K == 0) return st;
     if (ldx < (rows > 1 ? K : 0) || (rows > 1 && ldx > (INT64_MAX >> 4) / rows)) return LPGEMM_ERR_INVALID_ARG;
-    const int64_t units = ceil_div(K, kMxUnit);
-    const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(rows * units * 16, 256), 1 << 20);
-    uint32_t *c = reinterpret_cast<uint32_t *>(codes);
     (void)hipGetLastError();
     switch (f) {
-    case OUT_F32:
-        hipLaunchKernelGGL((mxfp4_quantize_kernel<OUT_F32>), dim3(blocks), dim3(256), 0, stream, X, ldx, c, scales, rows, K, units);
-        break;
-    case OUT_BF16:
-        hipLaunchKernelGGL((mxfp4_quantize_kernel<OUT_BF16>), dim3(blocks), dim3(256), 0, stream, X, ldx, c, scales, rows, K, units);
-        break;
-    default:
-        hipLaunchKernelGGL((mxfp4_quantize_kernel<OUT_F16>), dim3(blocks), dim3(256), 0, stream, X, ldx, c, scales, rows, K, units);
+    case OUT_F32: return launch_quantize<OUT_F32>(X, ldx, codes, scales, rows, K, stream);
+    case OUT_BF16: return launch_quantize<OUT_BF16>(X, ldx, codes, scales, rows, K, stream);
+    default: return launch_quantize<OUT_F16>(X, ldx, codes, scales, rows, K, stream);
     }
-    return launched();
 }
 
 lpgemm_status lpgemm_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, void *Y, lpgemm_out_dtype y_dtype,
@@ -163,21 +184,12 @@ lpgemm_status lpgemm_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scale
     const int f = format_of(y_dtype);
     const lpgemm_status st = check_values(Y, codes, scales, f, rows, K);
     if (st != LPGEMM_OK || rows == 0 || K == 0) return st;
-    const int64_t units = ceil_div(K, kMxUnit);
-    const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(rows * units * 16, 256), 1 << 20);
-    const uint32_t *c = reinterpret_cast<const uint32_t *>(codes);
     (void)hipGetLastError();
     switch (f) {
-    case OUT_F32:
-        hipLaunchKernelGGL((mxfp4_dequantize_kernel<OUT_F32>), dim3(blocks), dim3(256), 0, stream, c, scales, Y, rows, K, units);
-        break;
-    case OUT_BF16:
-        hipLaunchKernelGGL((mxfp4_dequantize_kernel<OUT_BF16>), dim3(blocks), dim3(256), 0, stream, c, scales, Y, rows, K, units);
-        break;
-    default:
-        hipLaunchKernelGGL((mxfp4_dequantize_kernel<OUT_F16>), dim3(blocks), dim3(256), 0, stream, c, scales, Y, rows, K, units);
+    case OUT_F32: return launch_dequantize<OUT_F32>(codes, scales, Y, rows, K, stream);
+    case OUT_BF16: return launch_dequantize<OUT_BF16>(codes, scales, Y, rows, K, stream);
+    default: return launch_dequantize<OUT_F16>(codes, scales, Y, rows, K, stream);
     }
-    return launched();
 }
 
 lpgemm_status lpgemm_mxfp4(const uint8_t *A, const uint8_t *SFA, const uint8_t *B, const uint8_t *SFB, void *D,

@@ -19,103 +19,227 @@ constexpr int kMxUnitCodes = 64;    // code bytes per unit
 constexpr int kMxUnitScales = 4;    // scale bytes per unit
 constexpr int kMxUnitE8M0 = 127;    // scale byte of 1.0
 
-// e2m1 code (3 bits) of a magnitude m >= 0, nearest, ties to the even code.
-__device__ __forceinline__ uint32_t e2m1_code(float m)
-{
-    return (uint32_t)(m > 0.25f) + (uint32_t)(m >= 0.75f) + (uint32_t)(m > 1.25f) + (uint32_t)(m >= 1.75f) +
-           (uint32_t)(m > 2.5f) + (uint32_t)(m >= 3.5f) + (uint32_t)(m > 5.0f);
-}
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 mx_bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 mx_f16x2 __attribute__((ext_vector_type(2)));
+typedef float mx_f32x2 __attribute__((ext_vector_type(2)));
 
-// 2^(s - 127) of an e8m0 byte (255: NaN); s = 0 is subnormal in binary32.
-__device__ __forceinline__ float e8m0_value(uint32_t s)
-{
-    return s == 255u ? __uint_as_float(0x7FC00000u) : s == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(s << 23);
-}
+// The scale operand of the fp4 conversions for an e8m0 byte below 255: they
+// take 2^(s - 127) from the exponent field.
+__device__ __forceinline__ float mx_scale(uint32_t s) { return __uint_as_float(s == 0u ? 0x00400000u : s << 23); }
 
-// Value of an e2m1 code: 0, 0.5, 1, 1.5, 2, 3, 4, 6 with the sign in bit 3.
-__device__ __forceinline__ float e2m1_value(uint32_t c)
+// 16 bytes at any address of the element's alignment (global memory takes
+// unaligned vector accesses).
+__device__ __forceinline__ u32x4 mx_load16(const void *p)
 {
-    const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-    const uint32_t mag = e ? ((126u + e) << 23) | (m << 22) : (m ? 0x3F000000u : 0u);
-    return __uint_as_float(mag | ((c & 8u) << 28));
+    u32x4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
 }
+__device__ __forceinline__ void mx_store16(void *p, u32x4 v) { __builtin_memcpy(p, &v, 16); }
 
-// An input value as binary32 (exact): IN is OUT_F32, OUT_BF16 or OUT_F16.
+// Eight values of a row from k0 on, zeros from K on: IN is OUT_F32, OUT_BF16
+// or OUT_F16; 16-bit types in w[0].
 template <int IN>
-__device__ __forceinline__ float mx_load(const void *x, int64_t i)
+__device__ __forceinline__ void mx_load8(const void *x, int64_t at, int left, u32x4 (&w)[2])
 {
-    if (IN == OUT_F32) return static_cast<const float *>(x)[i];
-    const uint16_t h = static_cast<const uint16_t *>(x)[i];
-    if (IN == OUT_BF16) return __uint_as_float((uint32_t)h << 16);
-    return (float)__builtin_bit_cast(_Float16, h);
-}
-
-// One thread per 8 values (4 code bytes); four neighbouring lanes share a
-// block and its maximum.
-template <int IN>
-__global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const void *__restrict__ X, int64_t ldx,
-                                                             uint32_t *__restrict__ codes,
-                                                             uint8_t *__restrict__ scales, int64_t rows,
-                                                             int64_t K, int64_t units)
-{
-    const int64_t total = rows * units * 16;  // threads with work; a multiple of 16
-    const int64_t step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
-        const int64_t row = i / (units * 16);
-        const int64_t k0 = (i - row * units * 16) * 8;
-        float x[8];
-        uint32_t a = 0;
+    w[0] = w[1] = u32x4{0, 0, 0, 0};
+    if (IN == OUT_F32) {
+        const float *p = static_cast<const float *>(x) + at;
+        if (left >= 8) {
+            w[0] = mx_load16(p);
+            w[1] = mx_load16(p + 4);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[j] = k0 + j < K ? mx_load<IN>(X, row * ldx + k0 + j) : 0.f;
-            a = max(a, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+            for (int j = 0; j < 7; ++j)
+                if (j < left) w[j / 4][j % 4] = __float_as_uint(p[j]);
         }
-        a = max(a, (uint32_t)__shfl_xor((int)a, 1));
-        a = max(a, (uint32_t)__shfl_xor((int)a, 2));
-        const uint32_t E = a >> 23;
-        const bool whole_pad = (k0 & ~(int64_t)31) >= K;
-        const uint32_t s = E == 255u ? 255u : whole_pad ? (uint32_t)kMxUnitE8M0 : max(E, 2u) - 2u;
-        // 2^(127 - s): normal for every s <= 252, so the products below are exact
-        // except where they fall far under 0.25
-        const float inv = __uint_as_float((254u - min(s, 252u)) << 23);
-        uint32_t out = 0;
-        if (s != 255u) {
+    } else {
+        const uint16_t *p = static_cast<const uint16_t *>(x) + at;
+        if (left >= 8) {
+            w[0] = mx_load16(p);
+        } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float m = fabsf(x[j]) * inv;
-                out |= (e2m1_code(m) | ((__float_as_uint(x[j]) >> 28) & 8u)) << (4 * j);
-            }
+            for (int j = 0; j < 7; ++j)
+                if (j < left) w[0][j / 2] |= (uint32_t)p[j] << (16 * (j % 2));
         }
-        codes[i] = out;
-        if ((i & 3) == 0) scales[i >> 2] = (uint8_t)s;
     }
 }
 
-// One thread per 8 values.
+// Largest magnitude of the eight as its bits: they order as the values do.
+template <int IN>
+__device__ __forceinline__ uint32_t mx_largest(const u32x4 (&w)[2])
+{
+    uint32_t a = 0;
+    if (IN == OUT_F32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a = max(a, w[j / 4][j % 4] & 0x7FFFFFFFu);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a = max(a, max(w[0][j] & 0x7FFFu, (w[0][j] >> 16) & 0x7FFFu));
+    }
+    return a;
+}
+
+// Exponent field in binary32 of the magnitude with these bits.
+template <int IN>
+__device__ __forceinline__ uint32_t mx_exponent(uint32_t a)
+{
+    if (IN == OUT_F32) return a >> 23;
+    if (IN == OUT_BF16) return a >> 7;
+    return __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)a)) >> 23;
+}
+
+// Eight e2m1 codes of the values over 2^(s - 127): the conversion divides,
+// rounds to nearest even and takes what is beyond 6 to 6.
+template <int IN>
+__device__ __forceinline__ uint32_t mx_codes(const u32x4 (&w)[2], float scale)
+{
+    uint32_t c = 0;
+    if (IN == OUT_F32) {
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(w[0][0]), __uint_as_float(w[0][1]), scale, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(w[0][2]), __uint_as_float(w[0][3]), scale, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(w[1][0]), __uint_as_float(w[1][1]), scale, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(w[1][2]), __uint_as_float(w[1][3]), scale, 3);
+    } else {
+        // scalars first: a bit cast of a vector's element takes the vector's first
+        const uint32_t d0 = w[0][0], d1 = w[0][1], d2 = w[0][2], d3 = w[0][3];
+        if (IN == OUT_BF16) {
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(mx_bf16x2, d0), scale, 0);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(mx_bf16x2, d1), scale, 1);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(mx_bf16x2, d2), scale, 2);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(mx_bf16x2, d3), scale, 3);
+        } else {
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(mx_f16x2, d0), scale, 0);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(mx_f16x2, d1), scale, 1);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(mx_f16x2, d2), scale, 2);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(mx_f16x2, d3), scale, 3);
+        }
+    }
+    return c;
+}
+
+// A workgroup takes 256 J items of eight values, neighbouring ones at a time;
+// an item is four code bytes, and four neighbouring lanes share a block and
+// its maximum.  `items` = 16 units of a row.
+struct MxItem {
+    int64_t row;
+    int32_t k0;
+};
+__device__ __forceinline__ MxItem mx_item(int64_t row0, uint32_t rest, uint32_t items)
+{
+    const uint32_t rows = rest / items;
+    return MxItem{row0 + rows, (int32_t)(8 * (rest - rows * items))};
+}
+
+template <int IN, int J>
+__global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const void *__restrict__ X, int64_t ldx,
+                                                             uint32_t *__restrict__ codes,
+                                                             uint8_t *__restrict__ scales, int64_t rows,
+                                                             int32_t K, uint32_t items)
+{
+    const int64_t total = rows * items;  // a multiple of 16
+    const int64_t first = (int64_t)blockIdx.x * (256 * J);
+    const int64_t row0 = first / items;
+    const uint32_t rest0 = (uint32_t)(first - row0 * items);
+    u32x4 w[J][2];
+    bool pad[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const uint32_t local = 256 * j + threadIdx.x;
+        const MxItem it = mx_item(row0, rest0 + local, items);
+        pad[j] = (it.k0 & ~31) >= K;
+        mx_load8<IN>(X, it.row * ldx + it.k0, first + local < total ? K - it.k0 : 0, w[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int64_t i = first + 256 * j + threadIdx.x;
+        uint32_t a = mx_largest<IN>(w[j]);
+        a = max(a, (uint32_t)__shfl_xor((int)a, 1));
+        a = max(a, (uint32_t)__shfl_xor((int)a, 2));
+        const uint32_t E = mx_exponent<IN>(a);
+        const uint32_t s = E == 255u ? 255u : pad[j] ? (uint32_t)kMxUnitE8M0 : max(E, 2u) - 2u;
+        const uint32_t c = s == 255u ? 0u : mx_codes<IN>(w[j], mx_scale(s));
+        if (i < total) {
+            codes[i] = c;
+            if ((i & 3) == 0) scales[i >> 2] = (uint8_t)s;
+        }
+    }
+}
+
+// Eight values of a code dword as OUT, times 2^(s - 127); s = 255: NaN.
 template <int OUT>
+__device__ __forceinline__ void mx_values(uint32_t c, uint32_t s, u32x4 (&w)[2])
+{
+    const float scale = mx_scale(s);
+    if (OUT == OUT_F32) {
+#define LPGEMM_MX_PAIR(q)                                                                     \
+        {                                                                                     \
+            const mx_f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, q);          \
+            w[(q) / 2][2 * ((q) % 2)] = s == 255u ? 0x7FC00000u : __float_as_uint(v.x);        \
+            w[(q) / 2][2 * ((q) % 2) + 1] = s == 255u ? 0x7FC00000u : __float_as_uint(v.y);    \
+        }
+        LPGEMM_MX_PAIR(0) LPGEMM_MX_PAIR(1) LPGEMM_MX_PAIR(2) LPGEMM_MX_PAIR(3)
+#undef LPGEMM_MX_PAIR
+    } else if (OUT == OUT_BF16) {
+        w[0] = u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 0)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 1)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3))};
+        if (s == 255u) w[0] = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+    } else {
+        w[0] = u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 0)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 1)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 2)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 3))};
+        if (s == 255u) w[0] = u32x4{0x7E007E00u, 0x7E007E00u, 0x7E007E00u, 0x7E007E00u};
+    }
+}
+
+template <int OUT, int J>
 __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const uint32_t *__restrict__ codes,
                                                                const uint8_t *__restrict__ scales,
-                                                               void *__restrict__ Y, int64_t rows, int64_t K,
-                                                               int64_t units)
+                                                               void *__restrict__ Y, int64_t rows, int32_t K,
+                                                               uint32_t items)
 {
-    const int64_t total = rows * units * 16;
-    const int64_t step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
-        const int64_t row = i / (units * 16);
-        const int64_t k0 = (i - row * units * 16) * 8;
-        const uint32_t c = codes[i];
-        const float S = e8m0_value(scales[i >> 2]);
+    const int64_t total = rows * items;
+    const int64_t first = (int64_t)blockIdx.x * (256 * J);
+    const int64_t row0 = first / items;
+    const uint32_t rest0 = (uint32_t)(first - row0 * items);
+    uint32_t c[J], s[J];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (k0 + j >= K) break;
-            float v = e2m1_value((c >> (4 * j)) & 15u) * S;
-            // the product itself is converted: folded into one operation with the
-            // conversion to fp16 it would lose the sign of a result that rounds to zero
-            asm volatile("" : "+v"(v));
-            if (OUT == OUT_F32)
-                static_cast<float *>(Y)[row * K + k0 + j] = v;
-            else
-                static_cast<uint16_t *>(Y)[row * K + k0 + j] = (uint16_t)out_bits<OUT>(v);
+    for (int j = 0; j < J; ++j) {
+        const int64_t i = min(first + 256 * j + threadIdx.x, total - 1);
+        c[j] = codes[i];
+        s[j] = scales[i >> 2];
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const uint32_t local = 256 * j + threadIdx.x;
+        const MxItem it = mx_item(row0, rest0 + local, items);
+        const int left = first + local < total ? K - it.k0 : 0;
+        u32x4 w[2];
+        mx_values<OUT>(c[j], s[j], w);
+        const int64_t at = it.row * K + it.k0;
+        if (OUT == OUT_F32) {
+            float *p = static_cast<float *>(Y) + at;
+            if (left >= 8) {
+                mx_store16(p, w[0]);
+                mx_store16(p + 4, w[1]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 7; ++k)
+                    if (k < left) p[k] = __uint_as_float(w[k / 4][k % 4]);
+            }
+        } else {
+            uint16_t *p = static_cast<uint16_t *>(Y) + at;
+            if (left >= 8) {
+                mx_store16(p, w[0]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 7; ++k)
+                    if (k < left) p[k] = (uint16_t)(w[0][k / 2] >> (16 * (k % 2)));
+            }
         }
     }
 }
