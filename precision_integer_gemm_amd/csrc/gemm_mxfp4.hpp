@@ -96,6 +96,12 @@ __device__ __forceinline__ void mx_dma16(i32x4 rsrc, uint32_t voffset, uint32_t 
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                  : : "v"(voffset), "s"(rsrc), "s"(lds_base) : "memory", "m0");
 }
+// mx_dma16 of data that is read once: it need not stay in the caches.
+__device__ __forceinline__ void mx_dma16_nt(i32x4 rsrc, uint32_t voffset, uint32_t lds_base)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds"
+                 : : "v"(voffset), "s"(rsrc), "s"(lds_base) : "memory", "m0");
+}
 __device__ __forceinline__ void mx_dma4(i32x4 rsrc, uint32_t voffset, uint32_t lds_base)
 {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
@@ -110,6 +116,53 @@ __device__ __forceinline__ uint32_t mx_pack2(float a, float b)
     const mx_f32x2 v = {a, b};
     if (OUT == OUT_BF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, mx_bf16x2));
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, mx_f16x2));
+}
+
+// Row tiles of `high` rows before each group, summed into cum[0 .. E], and
+// their number: thread t takes groups t P .. t P + P - 1.  cum has WAVES words
+// more for the waves' sums.
+template <int WAVES>
+__device__ __forceinline__ int mx_tiles_before(const MxArgs &g, int high, int32_t *cum)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int32_t *part = cum + g.E + 1;
+    const int P = (g.E + 64 * WAVES - 1) / (64 * WAVES);
+    int sum = 0;
+    for (int i = 0; i < P; ++i) {
+        int b = 0, f = 0;
+        if (tid * P + i < g.E) mx_group(g, tid * P + i, b, f);
+        sum += (f - b + high - 1) / high;
+    }
+    int run = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(run, d);
+        if (lane >= d) run += o;
+    }
+    if (lane == 63) part[wave] = run;
+    __syncthreads();
+    int before = run - sum;
+    for (int w = 0; w < wave; ++w) before += part[w];
+    for (int i = 0; i < P; ++i) {
+        const int e = tid * P + i;
+        if (e >= g.E) break;
+        int b, f;
+        mx_group(g, e, b, f);
+        cum[e] = before;
+        before += (f - b + high - 1) / high;
+        if (e == g.E - 1) cum[g.E] = before;
+    }
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(cum[g.E]);
+}
+
+// The group that row tile rt belongs to: the last that begins at or before it.
+__device__ __forceinline__ int mx_group_of(int rt, int E, const int32_t *cum)
+{
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+    for (int i = 0; i < E; i += 64) n += (int)__popcll(__ballot(i + lane < E && cum[i + lane] <= rt));
+    return __builtin_amdgcn_readfirstlane(n - 1);
 }
 
 // A workgroup of four waves (2 x 2) computes tiles of 64 FM x 64 FN, FM = 1 ..
@@ -153,42 +206,7 @@ __global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(
     const uint32_t ldc = (uint32_t)U * kMxUnitCodes, lds_ = (uint32_t)U * kMxUnitScales;
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(smem);
 
-    // Row tiles of every group, summed: thread t takes groups t P .. t P + P - 1.
-    int total_rt;
-    if (g.offsets == nullptr) {
-        total_rt = (g.R + 64 * FN - 1) / (64 * FN);
-    } else {
-        int32_t *part = cum + g.E + 1;
-        const int P = (g.E + 255) / 256;
-        int sum = 0;
-        for (int i = 0; i < P; ++i) {
-            const int e = tid * P + i;
-            int b = 0, f = 0;
-            if (e < g.E) mx_group(g, e, b, f);
-            sum += (f - b + 64 * FN - 1) / (64 * FN);
-        }
-        int run = sum;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int o = __shfl_up(run, d);
-            if (lane >= d) run += o;
-        }
-        if (lane == 63) part[wave] = run;
-        __syncthreads();
-        int before = run - sum;
-        for (int w = 0; w < wave; ++w) before += part[w];
-        for (int i = 0; i < P; ++i) {
-            const int e = tid * P + i;
-            if (e >= g.E) break;
-            int b, f;
-            mx_group(g, e, b, f);
-            cum[e] = before;
-            before += (f - b + 64 * FN - 1) / (64 * FN);
-            if (e == g.E - 1) cum[g.E] = before;
-        }
-        __syncthreads();
-        total_rt = __builtin_amdgcn_readfirstlane(cum[g.E]);
-    }
+    const int total_rt = g.offsets == nullptr ? (g.R + 64 * FN - 1) / (64 * FN) : mx_tiles_before<4>(g, 64 * FN, cum);
     const int total = total_rt * tiles_n;
     const int whole = total - total % xcds;
 
@@ -201,10 +219,7 @@ __global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(
         e = 0;
         if (g.offsets != nullptr) {
             const int rt = id / tiles_n;
-            int n = 0;
-            for (int i = 0; i < g.E; i += 64)
-                n += (int)__popcll(__ballot(i + lane < g.E && cum[i + lane] <= rt));
-            e = __builtin_amdgcn_readfirstlane(n - 1);
+            e = mx_group_of(rt, g.E, cum);
             first = __builtin_amdgcn_readfirstlane(cum[e]);
             mx_group(g, e, begin, end);
         }
@@ -458,6 +473,270 @@ __global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(
         // whole tiles issue one store per 16 bytes and lane; others count as none
         const bool full = tm0 + 64 * tfm <= tm1 && tn0 + T::BN <= g.N;
         pending = full && (OUT == OUT_F32 ? g.N % 4 == 0 : wide) ? tfm * FN * (OUT == OUT_F32 ? 4 : 2) : 0;
+    }
+}
+
+// ---- narrow kernel -------------------------------------------------------------
+// Few rows of A: bound by reading B once.  A workgroup of eight waves takes
+// strips of 16 rows of B; KW neighbouring waves split a strip's K, and 8 / KW
+// strips are worked on at a time.  Every wave streams its own part: a stage is
+// 16 rows x 4 units (256 contiguous bytes a row, 4 KB of codes and 256 bytes of
+// scales) copied straight into the wave's own ring of D slots, so no wave
+// waits for another's copies.  v_mfma_scale_f32_16x16x128 takes unit g of the
+// stage in lane group g and its block s in step s, one scale dword per lane and
+// stage.  In LDS chunk c of row r sits at c ^ r: the 16 rows of a fragment read
+// touch all banks once.  The KW partial tiles are added in LDS in a fixed
+// order, by the subgroup's waves in turn.
+//
+// A stays in registers (product: 16 FA rows, S stages a wave) or, where it
+// changes from strip to strip (grouped: tiles of up to 16 rows of one group,
+// gathered), comes through the ring beside B.
+constexpr int kMxNarrowWaves = 8;
+// Grouped calls keep what an item looks up in LDS: a load from memory would wait
+// behind the copies in flight.  A row number takes 16 bits there.
+constexpr int kMxNarrowRows = 896;
+constexpr int kMxNarrowGroups = 512;
+
+template <bool GROUPED>
+struct MxNarrow {
+    static constexpr int kSide = 4096 + 256;                     // a stage's codes and scales
+    static constexpr int kStage = kSide * (GROUPED ? 2 : 1);
+    static constexpr int kPer = GROUPED ? 10 : 5;                // copies of a stage
+    static constexpr int D = GROUPED ? 2 : 4;
+    static constexpr int kRing = kMxNarrowWaves * D * kStage;
+    static constexpr int kSums = 2 * kMxNarrowWaves * 64 * 16;
+    static constexpr int lds(int groups) { return kRing + kSums + (GROUPED ? 4 * (2 * groups + 1 + kMxNarrowWaves + kMxNarrowRows) : 0); }
+};
+
+typedef float mx_f32x4 __attribute__((ext_vector_type(4)));
+
+template <int FA, int S, bool GROUPED, int OUT>
+__global__ __launch_bounds__(64 * kMxNarrowWaves) void gemm_mxfp4_narrow_kernel(MxArgs g, int kw, int stages)
+{
+    static_assert(!GROUPED || (FA == 1 && S == 1), "grouped: one row tile, stages counted at run time");
+    using C = MxNarrow<GROUPED>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    mx_f32x4 *sums = reinterpret_cast<mx_f32x4 *>(smem + C::kRing);  // [2][waves][64]
+    int32_t *cum = reinterpret_cast<int32_t *>(smem + C::kRing + C::kSums);
+    uint32_t *bounds = reinterpret_cast<uint32_t *>(cum + g.E + 1 + kMxNarrowWaves);  // begin | end << 16
+    int32_t *index = reinterpret_cast<int32_t *>(bounds + g.E);
+
+    const int lane = threadIdx.x & 63, r16 = lane & 15, lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int part = wave % kw, sub = wave / kw, side_by_side = kMxNarrowWaves / kw;
+    const int U = g.U, strips = (g.N + 15) / 16;
+    const int n_stages = GROUPED ? stages : S;
+    const uint32_t ldc = (uint32_t)U * kMxUnitCodes, lds_ = (uint32_t)U * kMxUnitScales;
+    const uint32_t ring = (uint32_t)(wave * C::D * C::kStage);
+    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(smem) + ring;
+    const uint8_t *mine = smem + ring;
+
+    int items = strips;
+    if (GROUPED) {
+        if (g.rows != nullptr)
+            for (int i = threadIdx.x; i < g.R; i += 64 * kMxNarrowWaves) index[i] = g.rows[i];
+        for (int i = threadIdx.x; i < g.E; i += 64 * kMxNarrowWaves) {
+            int begin, end;
+            mx_group(g, i, begin, end);
+            bounds[i] = (uint32_t)begin | (uint32_t)end << 16;
+        }
+        items = mx_tiles_before<kMxNarrowWaves>(g, 16, cum) * strips;  // also the barrier behind the indices
+    }
+    const int rounds = (items - (int)blockIdx.x * side_by_side + (int)gridDim.x * side_by_side - 1) / ((int)gridDim.x * side_by_side);
+    if (rounds <= 0) return;
+
+    // This lane's part of each copy: rows 4 t + lg, chunk r16 ^ row of its 256
+    // bytes; scales: row lane / 4, unit lane % 4.
+    uint32_t b_off[4], chunk[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        chunk[t] = (uint32_t)(r16 ^ (4 * t + lg));
+        b_off[t] = (uint32_t)(4 * t + lg) * ldc + 16u * chunk[t];
+    }
+    const uint32_t sb_off = (uint32_t)(lane >> 2) * lds_ + 4u * (uint32_t)(lane & 3);
+
+    // Where an item's copies come from, set as its first stage is issued.
+    struct Item {
+        int strip, m0, m1;  // m0 < 0: none
+    };
+    auto item_of = [&](int round) __attribute__((always_inline)) {
+        Item it;
+        const int id = (round * (int)gridDim.x + (int)blockIdx.x) * side_by_side + sub;
+        it.m0 = id < items ? 0 : -1;
+        it.m1 = g.R;
+        it.strip = id;
+        if (GROUPED && id < items) {
+            const int e = mx_group_of(id / strips, g.E, cum);
+            const int first = __builtin_amdgcn_readfirstlane(cum[e]);
+            const uint32_t bound = __builtin_amdgcn_readfirstlane(bounds[e]);
+            const int begin = (int)(bound & 0xFFFFu), end = (int)(bound >> 16);
+            const int tiles = (end - begin + 15) / 16, in_group = id - first * strips;
+            // a strip's row tiles one after another: its later reads come from the caches
+            it.strip = e * strips + in_group / tiles;
+            it.m0 = begin + 16 * (in_group % tiles);
+            it.m1 = min(end, it.m0 + 16);
+        }
+        return it;
+    };
+    i32x4 rsrc_b, rsrc_sb, rsrc_a, rsrc_sa;
+    uint32_t a_off[4], sa_off;
+    if (GROUPED) {
+        rsrc_a = make_rsrc(g.A, (uint32_t)g.T * ldc);
+        rsrc_sa = make_rsrc(g.SFA, (uint32_t)g.T * lds_);
+    }
+    auto aim = [&](const Item &it) __attribute__((always_inline)) {
+        const int e = GROUPED ? it.strip / strips : 0, n0 = 16 * (it.strip - e * strips);
+        const int64_t brow = (int64_t)e * g.N + n0;
+        const uint32_t n = it.m0 < 0 ? 0u : (uint32_t)min(16, g.N - n0);
+        rsrc_b = make_rsrc(g.B + brow * ldc, n * ldc);
+        rsrc_sb = make_rsrc(g.SFB + brow * lds_, n * lds_);
+        if (GROUPED) {
+            auto row = [&](int r) __attribute__((always_inline)) -> int {
+                if (it.m0 < 0 || it.m0 + r >= it.m1) return -1;
+                const int at = g.rows == nullptr ? it.m0 + r : index[it.m0 + r];
+                return at < g.T ? at : -1;
+            };
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int at = row(4 * t + lg);
+                a_off[t] = at >= 0 ? (uint32_t)at * ldc + 16u * chunk[t] : kOutOfRange;
+            }
+            const int at = row(lane >> 2);
+            sa_off = at >= 0 ? (uint32_t)at * lds_ + 4u * (uint32_t)(lane & 3) : kOutOfRange;
+        }
+    };
+    auto issue = [&](int s, int slot) __attribute__((always_inline)) {
+        const int u0 = 4 * (part * n_stages + s);
+        const uint32_t base = lds0 + (uint32_t)(slot * C::kStage);
+        const uint32_t koff = (uint32_t)u0 * kMxUnitCodes, soff = (uint32_t)u0 * kMxUnitScales;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            mx_dma16_nt(rsrc_b, u0 + (int)(chunk[t] >> 2) < U ? b_off[t] + koff : kOutOfRange, base + (uint32_t)t * 1024u);
+        mx_dma4(rsrc_sb, u0 + (lane & 3) < U ? sb_off + soff : kOutOfRange, base + 4096u);
+        if (GROUPED) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                mx_dma16(rsrc_a, u0 + (int)(chunk[t] >> 2) < U ? a_off[t] + koff : kOutOfRange, base + C::kSide + (uint32_t)t * 1024u);
+            mx_dma4(rsrc_sa, u0 + (lane & 3) < U ? sa_off + soff : kOutOfRange, base + C::kSide + 4096u);
+        }
+    };
+
+    // A in registers: lane (r16, lg), stage s, unit lg: 64 code bytes, one scale dword.
+    i32x4 a[FA][S][4];
+    uint32_t sa[FA][S];
+    if (!GROUPED) {
+        const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(g.A, (uint32_t)g.R * ldc);
+        const __amdgpu_buffer_rsrc_t rsa = buffer_rsrc(g.SFA, (uint32_t)g.R * lds_);
+#pragma unroll
+        for (int f = 0; f < FA; ++f)
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const int u = 4 * (part * S + s) + lg;
+                const uint32_t row = (uint32_t)(16 * f + r16);
+                const bool in = u < U && (int)row < g.R;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    a[f][s][q] = buffer_load16(ra, in ? row * ldc + (uint32_t)u * kMxUnitCodes + 16u * q : kOutOfRange);
+                sa[f][s] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rsa, in ? row * lds_ + (uint32_t)u * kMxUnitScales : kOutOfRange, 0, 0);
+            }
+    }
+
+    // The copies run D stages ahead of the arithmetic, over the item borders.
+    int ahead_round = 0, ahead_stage = 0;
+    Item next = item_of(0), cur = next;
+    aim(next);
+    auto advance = [&](int slot) __attribute__((always_inline)) {
+        if (ahead_round < rounds) issue(ahead_stage, slot);
+        if (++ahead_stage == n_stages) {
+            ahead_stage = 0;
+            if (++ahead_round < rounds) {
+                next = item_of(ahead_round);
+                aim(next);
+            }
+        }
+    };
+    // grouped: the items between the arithmetic's and the copies' are looked up again
+#pragma unroll
+    for (int d = 0; d < C::D; ++d) advance(d);
+    if (!GROUPED) {
+        // A is waited for here, once
+#pragma unroll
+        for (int f = 0; f < FA; ++f)
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                asm volatile("" : "+v"(sa[f][s]));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) asm volatile("" : "+v"(a[f][s][q]));
+            }
+    }
+
+    int slot = 0, issued_left = rounds * n_stages;  // stages not yet contracted
+    for (int round = 0; round < rounds; ++round) {
+        mx_f32x4 acc[FA];
+#pragma unroll
+        for (int f = 0; f < FA; ++f) acc[f] = mx_f32x4{0.f, 0.f, 0.f, 0.f};
+        auto contract = [&](int s) __attribute__((always_inline)) {
+            // D stages are in flight while there are as many left
+            if (issued_left >= C::D)
+                wait_vmcnt<(C::D - 1) * C::kPer>();
+            else
+                wait_vmcnt<0>();
+            const uint8_t *base = mine + slot * C::kStage;
+            i32x4 b[4], ar[4];
+            uint32_t sar = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) b[q] = load16(base + r16 * 256 + 16 * ((4 * lg + q) ^ r16));
+            const uint32_t sb = *reinterpret_cast<const uint32_t *>(base + 4096 + 16 * r16 + 4 * lg);
+            if (GROUPED) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) ar[q] = load16(base + C::kSide + r16 * 256 + 16 * ((4 * lg + q) ^ r16));
+                sar = *reinterpret_cast<const uint32_t *>(base + C::kSide + 4096 + 16 * r16 + 4 * lg);
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read out before the slot is filled again
+            advance(slot);
+            slot = slot + 1 == C::D ? 0 : slot + 1;
+            --issued_left;
+#pragma unroll
+            for (int f = 0; f < FA; ++f) {
+#define LPGEMM_MX_STEP(q)                                                                                                 \
+    acc[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(b[q]), mx_operand(GROUPED ? ar[q] : a[f][s][q]), \
+                                                              acc[f], kMxFormat, kMxFormat, q, sb, q, GROUPED ? sar : sa[f][s]);
+                LPGEMM_MX_STEP(0) LPGEMM_MX_STEP(1) LPGEMM_MX_STEP(2) LPGEMM_MX_STEP(3)
+#undef LPGEMM_MX_STEP
+            }
+        };
+        if (GROUPED) {
+            for (int s = 0; s < n_stages; ++s) contract(0);
+        } else {
+#pragma unroll
+            for (int s = 0; s < S; ++s) contract(s);
+        }
+        cur = item_of(round);
+        auto store = [&](int f, const mx_f32x4 &x) __attribute__((always_inline)) {
+            const int e = GROUPED ? cur.strip / strips : 0;
+            const int m = cur.m0 + 16 * f + r16;
+            if (cur.m0 < 0 || m >= cur.m1) return;
+            Epilogue epi{g.D, nullptr, nullptr};
+            const float v[4] = {x.x, x.y, x.z, x.w};
+            store_row4f<OUT>(epi, m, g.N, 16 * (cur.strip - e * strips) + 4 * lg, v);
+        };
+        if (kw == 1) {
+#pragma unroll
+            for (int f = 0; f < FA; ++f) store(f, acc[f]);
+            continue;
+        }
+#pragma unroll
+        for (int f = 0; f < FA; ++f) {
+            // one row tile at a time through the sums' two halves in turn
+            const int half = (round * FA + f) & 1;
+            sums[(half * kMxNarrowWaves + wave) * 64 + lane] = acc[f];
+            lds_barrier();
+            if (part == (round * FA + f) % kw) {
+                mx_f32x4 x = sums[(half * kMxNarrowWaves + sub * kw) * 64 + lane];
+                for (int w = 1; w < kw; ++w) x += sums[(half * kMxNarrowWaves + sub * kw + w) * 64 + lane];
+                store(f, x);
+            }
+        }
     }
 }
 

@@ -114,6 +114,48 @@ lpgemm_status launch_simple(const MxArgs &g, hipStream_t stream)
     return launched();
 }
 
+template <int FA, int S, bool GROUPED, int OUT>
+lpgemm_status launch_narrow(const MxArgs &g, int kw, int stages, hipStream_t stream)
+{
+    using C = MxNarrow<GROUPED>;
+    static std::once_flag once[kMaxDevices];
+    static hipError_t err[kMaxDevices];
+    const auto kernel = &gemm_mxfp4_narrow_kernel<FA, S, GROUPED, OUT>;
+    const lpgemm_status st = allow_lds(kernel, C::lds(kMxNarrowGroups), once, err);
+    if (st != LPGEMM_OK) return st;
+    const int64_t items = ceil_div(g.N, 16) * (GROUPED ? ceil_div(g.R, 16) + std::min(g.E, g.R) : 1);
+    const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(items, kMxNarrowWaves / kw), compute_units());
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(64 * kMxNarrowWaves), C::lds(g.E), stream, g, kw, stages);
+    return launched();
+}
+
+// The narrow kernel's sizes: rows of a product, units of a wave's registers of
+// A, 32-bit offsets.
+constexpr int kNarrowRows = 32, kNarrowStages = 4;
+
+bool narrow_serves(const MxArgs &g)
+{
+    if (g.offsets != nullptr)
+        return g.R <= kMxNarrowRows && g.E <= kMxNarrowGroups && (int64_t)g.T * g.U * kMxUnitCodes <= INT32_MAX &&
+               ceil_div(g.N, 16) * (g.R + g.E) <= INT32_MAX / 16;
+    return g.R <= kNarrowRows && g.U <= 4 * kMxNarrowWaves * kNarrowStages && g.N <= INT32_MAX / 32;
+}
+
+template <int OUT>
+lpgemm_status launch_narrow_any(const MxArgs &g, hipStream_t stream)
+{
+    const int kw = g.U > 16 ? 8 : g.U > 8 ? 4 : g.U > 4 ? 2 : 1;
+    const int stages = (int)std::max<int64_t>(1, ceil_div(g.U, 4 * kw));
+    if (g.offsets != nullptr) return launch_narrow<1, 1, true, OUT>(g, kw, stages, stream);
+    if (g.R <= 16)
+        return stages == 1   ? launch_narrow<1, 1, false, OUT>(g, kw, 1, stream)
+               : stages == 2 ? launch_narrow<1, 2, false, OUT>(g, kw, 2, stream)
+                             : launch_narrow<1, 4, false, OUT>(g, kw, 4, stream);
+    return stages == 1   ? launch_narrow<2, 1, false, OUT>(g, kw, 1, stream)
+           : stages == 2 ? launch_narrow<2, 2, false, OUT>(g, kw, 2, stream)
+                         : launch_narrow<2, 4, false, OUT>(g, kw, 4, stream);
+}
+
 template <int OUT>
 lpgemm_status launch_product(const MxArgs &g, hipStream_t stream)
 {
@@ -122,11 +164,15 @@ lpgemm_status launch_product(const MxArgs &g, hipStream_t stream)
     int tile = 4 * tiles(256) >= 3 * cu ? 256 : tiles(128) >= cu ? 128 : 64;
     switch (forced_kernel()) {
     case LPGEMM_KERNEL_AUTO:
+        // grouped: up to eight rows a group on average
+        if (narrow_serves(g) && (g.offsets == nullptr || g.R <= 8 * (int64_t)g.E)) return launch_narrow_any<OUT>(g, stream);
+        break;
     case LPGEMM_KERNEL_TILED: break;
     case LPGEMM_KERNEL_GENERAL: return launch_simple<OUT>(g, stream);
     case LPGEMM_KERNEL_TILED_64: tile = 64; break;
     case LPGEMM_KERNEL_TILED_128: tile = 128; break;
     case LPGEMM_KERNEL_TILED_256: tile = 256; break;
+    case LPGEMM_KERNEL_SKINNY: return narrow_serves(g) ? launch_narrow_any<OUT>(g, stream) : LPGEMM_ERR_UNSUPPORTED;
     default: return LPGEMM_ERR_UNSUPPORTED;
     }
     // 32-bit row tile counts and offsets of a tile's rows

@@ -78,3 +78,57 @@ def test_tiled_many_groups(torch, forced, tile):  # noqa: F811
     sizes[700] = 300
     forced(TILED[tile])
     run_grouped(torch, rng, list(sizes), 40, 140, "float32")
+
+
+# ---- the narrow kernel ----------------------------------------------------------
+# K around each number of waves that split it (4, 8, 16 units) and of stages a wave holds; strips that end past N
+NARROW = [(1, 1, 1), (2, 15, 100), (16, 16, 512), (17, 17, 513), (32, 33, 640), (5, 100, 1024), (9, 250, 1025), (31, 48, 2048), (16, 4000, 2049),
+          (3, 300, 4096), (32, 5000, 4097), (16, 100, 8192), (20, 31, 8193), (1, 9000, 300), (32, 500, 16384), (7, 4, 16300), (12, 70000, 384)]
+
+
+@pytest.mark.parametrize("kind", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("M,N,K", NARROW)
+def test_narrow_product(torch, forced, kind, M, N, K):  # noqa: F811
+    rng = np.random.default_rng(M + N + K)
+    a, sa = R.random_operand(rng, M, K)
+    b, sb = R.random_operand(rng, N, K, center=117)
+    out, ok = guarded(torch, (M, N), dtypes(torch)[kind])
+    forced(L.KERNEL_SKINNY)
+    L.lpgemm_mxfp4(*dev(torch, a, sa, b, sb), out=out)
+    assert ok()
+    held(out, R.values(a, sa), R.values(b, sb), kind)
+
+
+@pytest.mark.parametrize("split", list(SPLITS))
+@pytest.mark.parametrize("N,K", [(96, 512), (301, 2897), (600, 40), (40, 9000), (17, 1100)])
+def test_narrow_grouped(torch, forced, split, N, K):  # noqa: F811
+    if np.sum(SPLITS[split]) > 896:
+        pytest.skip("more rows than the narrow kernel takes")
+    forced(L.KERNEL_SKINNY)
+    run_grouped(torch, np.random.default_rng(N), SPLITS[split], N, K, "bfloat16")
+
+
+@pytest.mark.parametrize("split", ["single rows", "empty ones", "skewed", "many", "one large"])
+def test_narrow_grouped_gathered_rows(torch, forced, split):  # noqa: F811
+    rng = np.random.default_rng(9)
+    rows = rng.integers(0, 50, int(np.sum(SPLITS[split])))
+    rows[::7], rows[3::11], rows[5::13], rows[6::17] = -1, 50, 2 ** 31 - 1, -2 ** 31
+    forced(L.KERNEL_SKINNY)
+    out = run_grouped(torch, rng, SPLITS[split], 200, 700, "float32", T=50, rows=rows)
+    assert not out[::7].any()
+
+
+def test_narrow_many_groups(torch, forced):  # noqa: F811
+    rng = np.random.default_rng(11)
+    sizes = rng.choice([0, 0, 0, 1, 2], 512)
+    sizes[300] = 60
+    forced(L.KERNEL_SKINNY)
+    run_grouped(torch, rng, list(sizes), 40, 140, "float32")
+
+
+def test_narrow_refuses_what_it_does_not_serve(torch, forced):  # noqa: F811
+    forced(L.KERNEL_SKINNY)
+    z = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    for M, U in ((33, 4), (4, 129)):
+        with pytest.raises(L.LpgemmError):
+            L.lpgemm_mxfp4(z(M, 64 * U), z(M, 4 * U), z(8, 64 * U), z(8, 4 * U))
