@@ -144,8 +144,21 @@ bool narrow_serves(const MxArgs &g)
 template <int OUT>
 lpgemm_status launch_narrow_any(const MxArgs &g, hipStream_t stream)
 {
-    const int kw = g.U > 16 ? 8 : g.U > 8 ? 4 : g.U > 4 ? 2 : 1;
-    const int stages = (int)std::max<int64_t>(1, ceil_div(g.U, 4 * kw));
+    // Waves to a strip: a strip costs its stages and 1.2 more for its sums and
+    // what leads to it, so fewer waves for many strips, more where a wave has
+    // one.  MI355X, 24 groups of 4096 x 4096: 59.8 us with 8 waves, 45.7 with 4,
+    // 37.0 with 2; 16 x 28672 x 8192: 26.4 us with 8, 24.0 with 4.
+    const int64_t strips = ceil_div(g.N, 16) * (g.offsets ? std::min(g.E, g.R) : 1);
+    int kw = 8, stages = 1;
+    int64_t least = INT64_MAX;
+    for (int w = kMxNarrowWaves; w > 0; w /= 2) {
+        const int64_t s = std::max<int64_t>(1, ceil_div(g.U, 4 * w));
+        const int64_t cost = ceil_div(strips, (int64_t)compute_units() * (kMxNarrowWaves / w)) * (5 * s + 6);
+        if ((g.offsets == nullptr && s > kNarrowStages) || cost >= least) continue;
+        least = cost;
+        kw = w;
+        stages = (int)s;
+    }
     if (g.offsets != nullptr) return launch_narrow<1, 1, true, OUT>(g, kw, stages, stream);
     if (g.R <= 16)
         return stages == 1   ? launch_narrow<1, 1, false, OUT>(g, kw, 1, stream)
