@@ -470,14 +470,16 @@ def lpgemm_unpack_int4(packed, *, out=None, stream=None):
 # ---- microscaled 4-bit floating point ------------------------------------------
 # These calls take a few microseconds on the device for a token's work, so what
 # the host does before a launch is kept short.
-_mx = None  # torch, the library and the result types' codes, once both are loaded
+_mx = None  # torch, the library, the result types' codes and the native calls, once all are loaded
 
 
 def _mx_torch():
     global _mx
     if _mx is None:
         torch = _torch()
-        _mx = (torch, lib(), {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16, torch.float16: OUT_F16})
+        library = lib()
+        from . import _tensor_calls
+        _mx = (torch, library, {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16, torch.float16: OUT_F16}, _tensor_calls)
     return _mx[0]
 
 
@@ -542,7 +544,7 @@ def _check_mx(codes, scales, name: str, dim: int, device=None):
 
 
 def _mx_out(out, dtype, M, N, device):
-    torch, _, codes = _mx
+    torch, codes = _mx[0], _mx[2]
     if out is None:
         dtype = dtype or torch.bfloat16
         code = codes.get(dtype)
@@ -561,6 +563,10 @@ def lpgemm_mxfp4_quantize(x, *, codes=None, scales=None, stream=None):
     and one e8m0 scale byte per 32 values.  Rows of x may be strided (its last
     dimension is dense)."""
     torch = _mx_torch()
+    if codes is None and scales is None and stream is None:
+        made = _mx[3].quantize(x)
+        if made is not None:
+            return made
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     code = _mx[2].get(x.dtype)
@@ -598,6 +604,11 @@ def _check_shape(t, name: str, shape, device):
 def lpgemm_mxfp4_dequantize(codes, scales, K, *, dtype=None, out=None, stream=None):
     """The values [rows, K] that mxfp4 codes and scales stand for (bfloat16 by
     default; exact in float32 and bfloat16)."""
+    _mx_torch()
+    if out is None and stream is None:
+        made = _mx[3].dequantize(codes, scales, K, dtype)
+        if made is not None:
+            return made
     units = _mx_units(codes, scales, "codes", 2)
     if K < 0 or _units(K) != units:
         raise ValueError(f"K={K} does not fit {units} units of {MXFP4_UNIT} values")
@@ -619,6 +630,11 @@ def lpgemm_mxfp4(A, SFA, B, SFB, *, dtype=None, out=None, workspace="auto", stre
     """D[M,N] = A . B^T of mxfp4 operands (codes [M, 64 U] and [N, 64 U], scales
     [M, 4 U] and [N, 4 U]) with fp32 accumulation, as bfloat16 (default),
     float16 or float32; workspace as for lpgemm_int4_int4."""
+    _mx_torch()
+    if out is None and stream is None and isinstance(workspace, str) and workspace == "auto":
+        made = _mx[3].product(A, SFA, B, SFB, dtype)
+        if made is not None:
+            return made
     units = _mx_units(A, SFA, "A", 2)
     device = A.device
     if _mx_units(B, SFB, "B", 2, device) != units:
@@ -639,6 +655,11 @@ def lpgemm_mxfp4_grouped(A, SFA, B, SFB, offsets, *, rows=None, dtype=None, out=
     offsets[e] <= i < offsets[e + 1], is row rows[i] of A times B[e]^T (rows
     None: row i; an index outside A's rows stands for zeros).  A codes [T, 64 U],
     B codes [E, N, 64 U], offsets int32 [E + 1] and rows int32 on the device."""
+    _mx_torch()
+    if out is None and stream is None:
+        made = _mx[3].grouped(A, SFA, B, SFB, offsets, rows, dtype)
+        if made is not None:
+            return made
     units = _mx_units(A, SFA, "A", 2)
     device = A.device
     if _mx_units(B, SFB, "B", 3, device) != units:

@@ -4,8 +4,9 @@
 
 compiles csrc/lpgemm_api.hip (which includes every integer and fp8 kernel) and
 csrc/mxfp4_api.hip (the microscaled 4-bit kernels) with hipcc into
-precision_integer_gemm_amd/_lpgemm.so, next to this file, and the measurement
-probe csrc/ceiling_probe.hip into _ceiling.so (loaded only by bench.py).
+precision_integer_gemm_amd/_lpgemm.so, next to this file, csrc/tensor_calls.cpp
+into the Python module _tensor_calls.so, and the measurement probe
+csrc/ceiling_probe.hip into _ceiling.so (loaded only by bench.py).
 """
 from __future__ import annotations
 
@@ -20,6 +21,8 @@ ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "lpgemm_api.hip")
 MX_SRC = os.path.join(PKG, "csrc", "mxfp4_api.hip")
 LIB = os.path.join(PKG, "_lpgemm.so")
+CALLS_SRC = os.path.join(PKG, "csrc", "tensor_calls.cpp")
+CALLS_LIB = os.path.join(PKG, "_tensor_calls.so")
 PROBE_SRC = os.path.join(PKG, "csrc", "ceiling_probe.hip")
 PROBE_LIB = os.path.join(PKG, "_ceiling.so")
 ARCH = "gfx950"
@@ -45,12 +48,32 @@ def command(out: str, src: str, *mode: str) -> list[str]:
     ]
 
 
+def calls_commands(obj: str, out: str) -> tuple[list[str], list[str]]:
+    """Compile and link commands of the Python module of the tensor calls: host
+    code against PyTorch's headers, linked to the library beside it."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+    headers = (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(rocm, "include"))
+    return ([
+        "g++", "-O2", "-std=c++17", "-c", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+        *(x for h in headers for x in ("-isystem", h)), "-o", obj, CALLS_SRC,
+    ], [
+        "g++", "-shared", "-o", out, obj, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip",
+        "-L", PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
+    ])
+
+
 def run(cmd: list[str], what: str, verbose: bool) -> None:
     proc = subprocess.run(cmd, capture_output=True, text=True)
     noise = "is not a recognized feature for this target"
     msgs = [l for l in (proc.stdout + proc.stderr).splitlines() if noise not in l]
     if proc.returncode != 0:
-        raise RuntimeError(f"hipcc failed on {what}:\n" + "\n".join(msgs))
+        raise RuntimeError(f"compiling {what} failed:\n" + "\n".join(msgs))
     if verbose and msgs:
         print("\n".join(msgs))
 
@@ -58,15 +81,20 @@ def run(cmd: list[str], what: str, verbose: bool) -> None:
 def build(verbose: bool = False) -> str:
     objects = [LIB + "." + os.path.basename(src) + ".o" for src in (SRC, MX_SRC)]
     jobs = [(command(o, src, "-c"), os.path.basename(src)) for o, src in zip(objects, (SRC, MX_SRC))]
+    calls_obj = CALLS_LIB + ".o"
+    calls_compile, calls_link = calls_commands(calls_obj, CALLS_LIB + ".tmp")
+    jobs.append((calls_compile, os.path.basename(CALLS_SRC)))
     jobs.append((command(PROBE_LIB + ".tmp", PROBE_SRC, "-shared"), os.path.basename(PROBE_SRC)))
     with ThreadPoolExecutor(len(jobs)) as pool:
         for done in [pool.submit(run, cmd, what, verbose) for cmd, what in jobs]:
             done.result()
     run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", LIB + ".tmp", *objects], "the library", verbose)
-    for o in objects:
-        os.remove(o)
     os.replace(PROBE_LIB + ".tmp", PROBE_LIB)
     os.replace(LIB + ".tmp", LIB)
+    run(calls_link, "the tensor calls", verbose)
+    os.replace(CALLS_LIB + ".tmp", CALLS_LIB)
+    for o in (*objects, calls_obj):
+        os.remove(o)
     return LIB
 
 
