@@ -96,6 +96,12 @@ __device__ __forceinline__ void mx_dma16(i32x4 rsrc, uint32_t voffset, uint32_t 
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                  : : "v"(voffset), "s"(rsrc), "s"(lds_base) : "memory", "m0");
 }
+// mx_dma16 from rsrc[voffset + soffset].
+__device__ __forceinline__ void mx_dma16_at(i32x4 rsrc, uint32_t voffset, uint32_t soffset, uint32_t lds_base)
+{
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 : : "v"(voffset), "s"(rsrc), "s"(soffset), "s"(lds_base) : "memory", "m0");
+}
 // mx_dma16 of data that is read once: it need not stay in the caches.
 __device__ __forceinline__ void mx_dma16_nt(i32x4 rsrc, uint32_t voffset, uint32_t lds_base)
 {
@@ -165,6 +171,65 @@ __device__ __forceinline__ int mx_group_of(int rt, int E, const int32_t *cum)
     return __builtin_amdgcn_readfirstlane(n - 1);
 }
 
+// Tile v of `total`: group e, rows [m0, m1) of D, height 64 fm, columns from
+// n0, for tiles of up to 64 FN rows and 64 FN columns.
+template <int FN>
+__device__ __forceinline__ void mx_find_tile(const MxArgs &g, int v, int total, int tiles_n, int xcds, const int32_t *cum, int &e,
+                                             int &m0, int &m1, int &n0, int &fm)
+{
+    // XCD-contiguous: workgroups v, v + 8, .. share an L2 and take neighbouring tiles
+    const int whole = total - total % xcds;
+    const int id = v < whole ? (v % xcds) * (whole / xcds) + v / xcds : v;
+    int begin = 0, end = g.R, first = 0;
+    e = 0;
+    if (g.offsets != nullptr) {
+        e = mx_group_of(id / tiles_n, g.E, cum);
+        first = __builtin_amdgcn_readfirstlane(cum[e]);
+        mx_group(g, e, begin, end);
+    }
+    begin = __builtin_amdgcn_readfirstlane(begin);
+    end = __builtin_amdgcn_readfirstlane(end);
+    const int blocks = (end - begin + 63) / 64, c = (blocks + FN - 1) / FN;  // of 64 rows; tiles
+    // bands of four row tiles, the band's tiles of one column together
+    const int in_group = id - first * tiles_n;
+    const int band = in_group / (4 * tiles_n), high = min(4, c - 4 * band);
+    const int in_band = in_group - band * 4 * tiles_n;
+    const int j = 4 * band + in_band % high;
+    n0 = in_band / high * 64 * FN;
+    // the group's blocks, shared out evenly
+    fm = blocks / c + (j < blocks % c ? 1 : 0);
+    m0 = begin + 64 * (j * (blocks / c) + min(j, blocks % c));
+    m1 = min(end, m0 + 64 * fm);
+}
+
+// One 32 x 32 block of D: row m, columns from nb; rows from m1 and columns from
+// N on are skipped.  bf16 and fp16 exchange halves where whole 16-byte stores
+// fit, so that a lane has eight neighbouring columns of its row.
+template <int OUT>
+__device__ __forceinline__ void mx_store_block(const MxArgs &g, const f32x16 &c, int m, int m1, int nb, int h)
+{
+    if (OUT != OUT_F32 && g.N % 8 == 0) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const uint32_t x0 = mx_pack2<OUT>(c[8 * q + 0], c[8 * q + 1]), x1 = mx_pack2<OUT>(c[8 * q + 2], c[8 * q + 3]);
+            const uint32_t y0 = mx_pack2<OUT>(c[8 * q + 4], c[8 * q + 5]), y1 = mx_pack2<OUT>(c[8 * q + 6], c[8 * q + 7]);
+            const auto s0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
+            const int n = nb + 16 * q + 8 * h;
+            if (m < m1 && n < g.N)
+                *reinterpret_cast<i32x4 *>(static_cast<uint16_t *>(g.D) + (int64_t)m * g.N + n) =
+                    i32x4{(int32_t)s0[0], (int32_t)s1[0], (int32_t)s0[1], (int32_t)s1[1]};
+        }
+    } else if (m < m1) {
+        Epilogue epi{g.D, nullptr, nullptr};
+#pragma unroll
+        for (int rg = 0; rg < 4; ++rg) {
+            const float x[4] = {c[4 * rg], c[4 * rg + 1], c[4 * rg + 2], c[4 * rg + 3]};
+            store_row4f<OUT>(epi, m, g.N, nb + 8 * rg + 4 * h, x);
+        }
+    }
+}
+
 // A workgroup of four waves (2 x 2) computes tiles of 64 FM x 64 FN, FM = 1 ..
 // FN chosen tile by tile from its group's rows, so a group wastes less than 64
 // rows whatever its size; a wave holds FM x FN blocks of 32 x 32.
@@ -208,34 +273,11 @@ __global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(
 
     const int total_rt = g.offsets == nullptr ? (g.R + 64 * FN - 1) / (64 * FN) : mx_tiles_before<4>(g, 64 * FN, cum);
     const int total = total_rt * tiles_n;
-    const int whole = total - total % xcds;
 
     // The current tile: group e, rows [m0, m1) of D, columns from n0, height 64 fm.
     int e = 0, m0 = 0, m1 = 0, n0 = 0, fm = 0;
     auto find = [&](int v) __attribute__((always_inline)) {
-        // XCD-contiguous: workgroups v, v + 8, .. share an L2 and take neighbouring tiles
-        const int id = v < whole ? (v % xcds) * (whole / xcds) + v / xcds : v;
-        int begin = 0, end = g.R, first = 0;
-        e = 0;
-        if (g.offsets != nullptr) {
-            const int rt = id / tiles_n;
-            e = mx_group_of(rt, g.E, cum);
-            first = __builtin_amdgcn_readfirstlane(cum[e]);
-            mx_group(g, e, begin, end);
-        }
-        begin = __builtin_amdgcn_readfirstlane(begin);
-        end = __builtin_amdgcn_readfirstlane(end);
-        const int blocks = (end - begin + 63) / 64, c = (blocks + FN - 1) / FN;  // of 64 rows; tiles
-        // bands of four row tiles, the band's tiles of one column together
-        const int in_group = id - first * tiles_n;
-        const int band = in_group / (4 * tiles_n), high = min(4, c - 4 * band);
-        const int in_band = in_group - band * 4 * tiles_n;
-        const int j = 4 * band + in_band % high;
-        n0 = in_band / high * T::BN;
-        // the group's blocks, shared out evenly
-        fm = blocks / c + (j < blocks % c ? 1 : 0);
-        m0 = begin + 64 * (j * (blocks / c) + min(j, blocks % c));
-        m1 = min(end, m0 + 64 * fm);
+        mx_find_tile<FN>(g, v, total, tiles_n, xcds, cum, e, m0, m1, n0, fm);
     };
 
     // Source offsets of this lane in each copy of a stage.
@@ -436,44 +478,266 @@ __global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(
             place();
             prologue();
         }
-        // Stores: bf16 and fp16 exchange halves so that a lane has eight
-        // neighbouring columns of one row, 16 bytes.
-        const bool wide = OUT != OUT_F32 && g.N % 8 == 0;
 #pragma unroll
         for (int f = 0; f < FN; ++f) {
             if (f >= tfm) break;
-            const int m = tm0 + (wm * tfm + f) * 32 + r32;
 #pragma unroll
-            for (int fn = 0; fn < FN; ++fn) {
-                const int nb = tn0 + (wn * FN + fn) * 32;
-                const f32x16 c = acc[fn][f];
-                if (wide) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const uint32_t x0 = mx_pack2<OUT>(c[8 * q + 0], c[8 * q + 1]), x1 = mx_pack2<OUT>(c[8 * q + 2], c[8 * q + 3]);
-                        const uint32_t y0 = mx_pack2<OUT>(c[8 * q + 4], c[8 * q + 5]), y1 = mx_pack2<OUT>(c[8 * q + 6], c[8 * q + 7]);
-                        const auto s0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
-                        const auto s1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
-                        const int n = nb + 16 * q + 8 * h;
-                        if (m < tm1 && n < g.N)
-                            *reinterpret_cast<i32x4 *>(static_cast<uint16_t *>(g.D) + (int64_t)m * g.N + n) =
-                                i32x4{(int32_t)s0[0], (int32_t)s1[0], (int32_t)s0[1], (int32_t)s1[1]};
-                    }
-                } else if (m < tm1) {
-                    Epilogue epi{g.D, nullptr, nullptr};
-#pragma unroll
-                    for (int rg = 0; rg < 4; ++rg) {
-                        const float x[4] = {c[4 * rg], c[4 * rg + 1], c[4 * rg + 2], c[4 * rg + 3]};
-                        store_row4f<OUT>(epi, m, g.N, nb + 8 * rg + 4 * h, x);
-                    }
-                }
-            }
+            for (int fn = 0; fn < FN; ++fn)
+                mx_store_block<OUT>(g, acc[fn][f], tm0 + (wm * tfm + f) * 32 + r32, tm1, tn0 + (wn * FN + fn) * 32, h);
         }
         if (v >= total) break;
         // whole tiles issue one store per 16 bytes and lane; others count as none
         const bool full = tm0 + 64 * tfm <= tm1 && tn0 + T::BN <= g.N;
-        pending = full && (OUT == OUT_F32 ? g.N % 4 == 0 : wide) ? tfm * FN * (OUT == OUT_F32 ? 4 : 2) : 0;
+        pending = full && g.N % 8 == 0 ? tfm * FN * (OUT == OUT_F32 ? 4 : 2) : 0;
     }
+}
+
+// ---- large tiles -----------------------------------------------------------
+// Tiles of 64 FM x 256, FM = 1 .. 4 by the group's rows, four waves (2 x 2) of
+// FM x 4 blocks of 32 x 32, one workgroup per compute unit.  A stage is two
+// units (256 k) as above.
+//
+// Each wave reads the next stage's fragments into registers while it
+// contracts this one: in step s (FM x 4 MFMAs on block s of every unit) all of
+// block s of its half of A and of B.  After the step's barrier these rows'
+// place in LDS is free, and the copies of the stage after the next go there:
+// four a wave and step (wave w serves half w % 2 of A or B), spread between
+// the MFMAs, with seven steps for them to arrive.  With all of a stage's
+// copies behind its last step, as the smaller tiles have them, the one wave of
+// a SIMD stood still for them: 8192^3 took 400 us.
+//
+// Scales come four units at a time: 16 bytes of every row for two stages, from
+// the row's last four units where fewer are left (U >= 4).  A scale past the
+// row is then another of that row's: it meets zero codes, and it is NaN only
+// where the row's results are anyway.
+struct MxLarge {
+    static constexpr int kSlot = 65536;                   // A's halves and B's halves, 16 KB each
+    static constexpr int kScales = 2 * kSlot;             // two slots of 8 KB
+    static constexpr int kTables = kScales + 2 * 8192;
+    static constexpr int lds(int groups) { return kTables + 4 * (groups + 1 + 4); }
+    static constexpr int kMinUnits = 4;
+};
+
+template <int OUT>
+__global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int tiles_n, int xcds)
+{
+    using C = MxLarge;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    int32_t *cum = reinterpret_cast<int32_t *>(smem + C::kTables);
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int r32 = lane & 31, h = lane >> 5;
+    const int U = g.U, pairs = (U + 3) / 4;  // of stages
+    const uint32_t ldc = (uint32_t)U * kMxUnitCodes, lds_ = (uint32_t)U * kMxUnitScales;
+    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(smem);
+
+    const int total_rt = g.offsets == nullptr ? (g.R + 255) / 256 : mx_tiles_before<4>(g, 256, cum);
+    const int total = total_rt * tiles_n;
+
+    // The current tile: group e, rows [m0, m1) of D, columns from n0, height 64 fm.
+    int e = 0, m0 = 0, m1 = 0, n0 = 0, fm = 0;
+    auto find = [&](int v) __attribute__((always_inline)) {
+        mx_find_tile<4>(g, v, total, tiles_n, xcds, cum, e, m0, m1, n0, fm);
+    };
+
+    // This wave's copies: half `wave % 2` of A (waves 0, 1) or B.
+    const bool of_b = wave >= 2;
+    const int half = wave & 1;
+    const uint32_t lds_mine = lds0 + (uint32_t)wave * 16384u;
+    const uint32_t lds_scales = lds0 + (uint32_t)C::kScales + (uint32_t)wave * 2048u;
+    i32x4 rsrc, rsrc_s;
+    uint32_t off[4][4], s_off[2];
+    int upper[2];  // unit of the stage that copies p = 0, 2 (1, 3) bring to this lane
+#pragma unroll
+    for (int p = 0; p < 2; ++p) upper[p] = ((lane & 7) ^ ((4 * p + (lane >> 4)) & 7)) >> 2;
+    auto place = [&]() __attribute__((always_inline)) {
+        const int64_t brow = (int64_t)e * g.N + n0;
+        const uint32_t nrows = (uint32_t)min(256, g.N - n0);
+        const bool gather = !of_b && g.rows != nullptr;
+        const int64_t arow = gather ? 0 : m0;
+        const uint32_t mrows = (uint32_t)(gather ? g.T : m1 - m0);
+        rsrc = make_rsrc(of_b ? g.B + brow * ldc : g.A + arow * ldc, (of_b ? nrows : mrows) * ldc);
+        rsrc_s = make_rsrc(of_b ? g.SFB + brow * lds_ : g.SFA + arow * lds_, (of_b ? nrows : mrows) * lds_);
+        const int blocks = of_b ? 4 : fm;  // of 32 rows in this half
+        // source row of row r of the half, or -1
+        auto row = [&](int r) __attribute__((always_inline)) -> int {
+            if (r >= 32 * blocks) return -1;
+            const int at = half * 32 * blocks + r;
+            if (!gather) return at;
+            const int i = m0 + at < m1 ? g.rows[m0 + at] : -1;
+            return i < g.T ? i : -1;
+        };
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int at = row(32 * s + 8 * p + (lane >> 3));
+                off[s][p] = at >= 0 ? (uint32_t)at * ldc + 16u * (uint32_t)((lane & 7) ^ ((4 * p + (lane >> 4)) & 7)) : kOutOfRange;
+            }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = row(64 * i + lane);
+            s_off[i] = at >= 0 ? (uint32_t)at * lds_ : kOutOfRange;
+        }
+    };
+    // Copy p of block s of stage k; stages and units past the row read zeros.
+    auto copy = [&](int s, int p, int k) __attribute__((always_inline)) {
+        const uint32_t o = upper[p & 1] < U - 2 * k ? off[s][p] : kOutOfRange;
+        mx_dma16_at(rsrc, o, (uint32_t)k * 128u, lds_mine + (uint32_t)((k & 1) * C::kSlot + s * 4096 + p * 1024));
+    };
+    auto copy_scales = [&](int i, int q) __attribute__((always_inline)) {
+        const uint32_t o = 4 * q < U ? s_off[i] : kOutOfRange;
+        mx_dma16_at(rsrc_s, o, (uint32_t)min(4 * q, U - 4) * 4u, lds_scales + (uint32_t)((q & 1) * 8192 + i * 1024));
+    };
+    auto prologue = [&]() __attribute__((always_inline)) {
+        copy_scales(0, 0);
+        copy_scales(1, 0);
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) copy(s & 3, p, s >> 2);
+    };
+
+    int v = blockIdx.x;
+    if (v >= total) return;
+    find(v);
+    place();
+    prologue();
+    int pending = 0;  // store instructions of the previous tile, at least
+
+    auto run_tile = [&](auto height) __attribute__((always_inline)) {
+        constexpr int FM = decltype(height)::value;
+        f32x16 acc[4][FM];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j) acc[i][j] = f32x16{};
+
+        struct Frags {
+            i32x4 a[4][4], b[4][4];  // [block][step]
+            uint32_t sa[4], sb[4];
+        };
+        Frags x, y;
+        const uint32_t at_a = (uint32_t)(wm * 16384 + r32 * 128), at_b = (uint32_t)((2 + wn) * 16384 + r32 * 128);
+        uint32_t at[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) at[t] = 16u * (uint32_t)((4 * h + t) ^ ((r32 >> 1) & 7));
+        // read j of block s of stage k: four fragments of B, four of A, their scales
+        constexpr int kReads = 10;
+        auto read = [&](Frags &f, int j, int s, int k) __attribute__((always_inline)) {
+            const uint8_t *slot = smem + (k & 1) * C::kSlot + s * 4096;
+            if (j < 4) {
+                f.b[s][j] = load16(slot + at_b + at[j]);
+            } else if (j < 8) {
+                if (s < FM) f.a[s][j - 4] = load16(slot + at_a + at[j - 4]);
+            } else {
+                const int q = k >> 1, i = min(2 * k + h - min(4 * q, U - 4), 3);
+                const uint8_t *sc = smem + C::kScales + (q & 1) * 8192 + (32 * s + r32) * 16 + 4 * i;
+                if (j == 8)
+                    f.sb[s] = *reinterpret_cast<const uint32_t *>(sc + (2 + wn) * 2048);
+                else if (s < FM)
+                    f.sa[s] = *reinterpret_cast<const uint32_t *>(sc + wm * 2048);
+            }
+        };
+
+        // stage 0 into registers, then its place to stage 2
+        if (pending >= 32)
+            wait_vmcnt<16 + 32>();
+        else if (pending >= 16)
+            wait_vmcnt<16 + 16>();
+        else
+            wait_vmcnt<16>();
+        lds_barrier();
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int j = 0; j < kReads; ++j) read(x, j, s, 0);
+        lds_barrier();
+#pragma unroll
+        for (int s = 0; s < 3; ++s) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) copy(s, p, 2);
+            if (s == 0) {
+                copy_scales(0, 1);
+                copy_scales(1, 1);
+            }
+        }
+
+        // Step S of stage k (cur: its fragments): the next stage's block S into
+        // nxt; copies of block S - 1 of the stage after that one's successor
+        // (step 0: of block 3 of the stage after the next), and of the scales.
+        // The wait leaves the last six steps' copies in flight: 24, and two of
+        // scales where step 1 of an odd stage is among them.
+        auto step = [&](auto index, auto parity, const Frags &cur, Frags &nxt, int k) __attribute__((always_inline)) {
+            constexpr int S = decltype(index)::value, ODD = decltype(parity)::value;
+            constexpr int kAt = 4 * ODD + S;
+            wait_vmcnt<(kAt == 4 || kAt == 5) ? 24 : 26>();
+            lds_barrier();
+            constexpr int kBlocks = 4 * FM, kCopies = (ODD && S == 1) ? 6 : 4;
+            constexpr int kPer = (kReads + kBlocks - 1) / kBlocks;
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const int fn = b / FM, f = b % FM;
+                acc[fn][f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(cur.b[fn][S]), mx_operand(cur.a[f][S]),
+                                                                             acc[fn][f], kMxFormat, kMxFormat, S, cur.sb[fn], S, cur.sa[f]);
+#pragma unroll
+                for (int j = 0; j < kReads; ++j)
+                    if (j / kPer == b) read(nxt, j, S, k + 1);
+#pragma unroll
+                for (int c = 0; c < kCopies; ++c)
+                    if (c * kBlocks / kCopies == b) {
+                        if (c >= 4)
+                            copy_scales(c - 4, (k + 3) >> 1);
+                        else if (S == 0)
+                            copy(3, c, k + 2);
+                        else
+                            copy(S - 1, c, k + 3);
+                    }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        using i0 = std::integral_constant<int, 0>;
+        using i1 = std::integral_constant<int, 1>;
+        using i2 = std::integral_constant<int, 2>;
+        using i3 = std::integral_constant<int, 3>;
+        for (int k = 0; k < 2 * pairs; k += 2) {
+            step(i0{}, i0{}, x, y, k);
+            step(i1{}, i0{}, x, y, k);
+            step(i2{}, i0{}, x, y, k);
+            step(i3{}, i0{}, x, y, k);
+            step(i0{}, i1{}, y, x, k + 1);
+            step(i1{}, i1{}, y, x, k + 1);
+            step(i2{}, i1{}, y, x, k + 1);
+            step(i3{}, i1{}, y, x, k + 1);
+        }
+        wait_vmcnt<0>();  // copies past the last stage
+
+        const int tm0 = m0, tm1 = m1, tn0 = n0;
+        v += (int)gridDim.x;
+        lds_barrier();  // every wave is done with the ring
+        if (v < total) {
+            find(v);
+            place();
+            prologue();
+        }
+#pragma unroll
+        for (int f = 0; f < FM; ++f)
+#pragma unroll
+            for (int fn = 0; fn < 4; ++fn)
+                mx_store_block<OUT>(g, acc[fn][f], tm0 + (wm * FM + f) * 32 + r32, tm1, tn0 + (wn * 4 + fn) * 32, h);
+        const bool full = tm0 + 64 * FM <= tm1 && tn0 + 256 <= g.N;
+        pending = full && g.N % 8 == 0 ? 4 * FM * (OUT == OUT_F32 ? 4 : 2) : 0;
+    };
+
+    while (v < total) {
+        if (fm == 4) run_tile(std::integral_constant<int, 4>{});
+        else if (fm == 3) run_tile(std::integral_constant<int, 3>{});
+        else if (fm == 2) run_tile(std::integral_constant<int, 2>{});
+        else run_tile(std::integral_constant<int, 1>{});
+    }
+    wait_vmcnt<0>();
 }
 
 // ---- narrow kernel -------------------------------------------------------------

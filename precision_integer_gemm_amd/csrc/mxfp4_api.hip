@@ -107,6 +107,21 @@ lpgemm_status launch_tiled(const MxArgs &g, hipStream_t stream)
 }
 
 template <int OUT>
+lpgemm_status launch_large(const MxArgs &g, hipStream_t stream)
+{
+    static std::once_flag once[kMaxDevices];
+    static hipError_t err[kMaxDevices];
+    const auto kernel = &gemm_mxfp4_large_kernel<OUT>;
+    const lpgemm_status st = allow_lds(kernel, MxLarge::lds(LPGEMM_MXFP4_MAX_GROUPS), once, err);
+    if (st != LPGEMM_OK) return st;
+    const int tiles_n = (int)ceil_div(g.N, 256);
+    const int64_t most = (ceil_div(g.R, 256) + (g.offsets ? std::min(g.E, g.R) : 0)) * tiles_n;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(most, compute_units())), dim3(256), MxLarge::lds(g.E), stream, g, tiles_n,
+                       kXcds);
+    return launched();
+}
+
+template <int OUT>
 lpgemm_status launch_simple(const MxArgs &g, hipStream_t stream)
 {
     const dim3 grid((unsigned)ceil_div(g.N, 128), (unsigned)std::min<int64_t>(ceil_div(g.R, 32), 65535), (unsigned)g.E);
@@ -190,6 +205,7 @@ lpgemm_status launch_product(const MxArgs &g, hipStream_t stream)
     }
     // 32-bit row tile counts and offsets of a tile's rows
     if (ceil_div(g.R, tile) + g.E > INT32_MAX / ceil_div(g.N, tile)) return LPGEMM_ERR_UNSUPPORTED;
+    if (tile == 256 && g.U >= MxLarge::kMinUnits) return launch_large<OUT>(g, stream);
     return tile == 256 ? launch_tiled<4, OUT>(g, stream) : tile == 128 ? launch_tiled<2, OUT>(g, stream) : launch_tiled<1, OUT>(g, stream);
 }
 
