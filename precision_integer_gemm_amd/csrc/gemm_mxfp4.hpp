@@ -511,9 +511,12 @@ __global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(
 // row is then another of that row's: it meets zero codes, and it is NaN only
 // where the row's results are anyway.
 struct MxLarge {
-    static constexpr int kSlot = 65536;                   // A's halves and B's halves, 16 KB each
-    static constexpr int kScales = 2 * kSlot;             // two slots of 8 KB
-    static constexpr int kTables = kScales + 2 * 8192;
+    // Codes: 32 KB for each half of A and of B, in it 8 KB for each block of 32
+    // rows, 4 KB a slot (a read's slot and block fit its offset field);
+    // scales: 4 KB for each half, 2 KB a slot.
+    static constexpr int kHalf = 32768, kBlock = 8192, kSlot = 4096;
+    static constexpr int kScales = 4 * kHalf, kScaleHalf = 4096, kScaleSlot = 2048;
+    static constexpr int kTables = kScales + 4 * kScaleHalf;
     static constexpr int lds(int groups) { return kTables + 4 * (groups + 1 + 4); }
     static constexpr int kMinUnits = 4;
 };
@@ -525,10 +528,18 @@ __global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int 
     extern __shared__ __align__(1024) uint8_t smem[];
     int32_t *cum = reinterpret_cast<int32_t *>(smem + C::kTables);
 
-    const int lane = threadIdx.x & 63;
+    // What depends on the lane is computed afresh where it is used, from an
+    // opaque copy of its number: kept through the K loop it would not fit the
+    // registers, and a spilled value that is read back waits for every copy
+    // in flight.
+    auto opaque_lane = [&]() __attribute__((always_inline)) {
+        int l = (int)threadIdx.x & 63;
+        asm volatile("" : "+v"(l));
+        return l;
+    };
+    const int lane0 = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 1, wn = wave & 1;
-    const int r32 = lane & 31, h = lane >> 5;
     const int U = g.U, pairs = (U + 3) / 4;  // of stages
     const uint32_t ldc = (uint32_t)U * kMxUnitCodes, lds_ = (uint32_t)U * kMxUnitScales;
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(smem);
@@ -545,14 +556,15 @@ __global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int 
     // This wave's copies: half `wave % 2` of A (waves 0, 1) or B.
     const bool of_b = wave >= 2;
     const int half = wave & 1;
-    const uint32_t lds_mine = lds0 + (uint32_t)wave * 16384u;
-    const uint32_t lds_scales = lds0 + (uint32_t)C::kScales + (uint32_t)wave * 2048u;
+    const uint32_t lds_mine = lds0 + (uint32_t)(wave * C::kHalf);
+    const uint32_t lds_scales = lds0 + (uint32_t)(C::kScales + wave * C::kScaleHalf);
     i32x4 rsrc, rsrc_s;
     uint32_t off[4][4], s_off[2];
     int upper[2];  // unit of the stage that copies p = 0, 2 (1, 3) bring to this lane
 #pragma unroll
-    for (int p = 0; p < 2; ++p) upper[p] = ((lane & 7) ^ ((4 * p + (lane >> 4)) & 7)) >> 2;
+    for (int p = 0; p < 2; ++p) upper[p] = ((lane0 & 7) ^ ((4 * p + (lane0 >> 4)) & 7)) >> 2;
     auto place = [&]() __attribute__((always_inline)) {
+        const int lane = opaque_lane();
         const int64_t brow = (int64_t)e * g.N + n0;
         const uint32_t nrows = (uint32_t)min(256, g.N - n0);
         const bool gather = !of_b && g.rows != nullptr;
@@ -585,11 +597,11 @@ __global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int 
     // Copy p of block s of stage k; stages and units past the row read zeros.
     auto copy = [&](int s, int p, int k) __attribute__((always_inline)) {
         const uint32_t o = upper[p & 1] < U - 2 * k ? off[s][p] : kOutOfRange;
-        mx_dma16_at(rsrc, o, (uint32_t)k * 128u, lds_mine + (uint32_t)((k & 1) * C::kSlot + s * 4096 + p * 1024));
+        mx_dma16_at(rsrc, o, (uint32_t)k * 128u, lds_mine + (uint32_t)(s * C::kBlock + (k & 1) * C::kSlot + p * 1024));
     };
     auto copy_scales = [&](int i, int q) __attribute__((always_inline)) {
         const uint32_t o = 4 * q < U ? s_off[i] : kOutOfRange;
-        mx_dma16_at(rsrc_s, o, (uint32_t)min(4 * q, U - 4) * 4u, lds_scales + (uint32_t)((q & 1) * 8192 + i * 1024));
+        mx_dma16_at(rsrc_s, o, (uint32_t)min(4 * q, U - 4) * 4u, lds_scales + (uint32_t)((q & 1) * C::kScaleSlot + i * 1024));
     };
     auto prologue = [&]() __attribute__((always_inline)) {
         copy_scales(0, 0);
@@ -609,6 +621,7 @@ __global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int 
 
     auto run_tile = [&](auto height) __attribute__((always_inline)) {
         constexpr int FM = decltype(height)::value;
+        const int lane = opaque_lane(), r32 = lane & 31, h = lane >> 5;
         f32x16 acc[4][FM];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -620,25 +633,31 @@ __global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int 
             uint32_t sa[4], sb[4];
         };
         Frags x, y;
-        const uint32_t at_a = (uint32_t)(wm * 16384 + r32 * 128), at_b = (uint32_t)((2 + wn) * 16384 + r32 * 128);
-        uint32_t at[4];
+        // this lane's place in a block of A's and B's halves: row r32, block t of unit h
+        uint32_t at_a[4], at_b[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) at[t] = 16u * (uint32_t)((4 * h + t) ^ ((r32 >> 1) & 7));
-        // read j of block s of stage k: four fragments of B, four of A, their scales
+        for (int t = 0; t < 4; ++t) {
+            const uint32_t at = (uint32_t)(r32 * 128 + 16 * ((4 * h + t) ^ ((r32 >> 1) & 7)));
+            at_a[t] = (uint32_t)(wm * C::kHalf) + at;
+            at_b[t] = (uint32_t)((2 + wn) * C::kHalf) + at;
+        }
+        const uint32_t at_sa = (uint32_t)(C::kScales + wm * C::kScaleHalf + r32 * 16);
+        const uint32_t at_sb = (uint32_t)(C::kScales + (2 + wn) * C::kScaleHalf + r32 * 16);
+        // read j of block s of stage k (its parity odd): four fragments of B, four of A, their scales
         constexpr int kReads = 10;
-        auto read = [&](Frags &f, int j, int s, int k) __attribute__((always_inline)) {
-            const uint8_t *slot = smem + (k & 1) * C::kSlot + s * 4096;
+        auto read = [&](Frags &f, int j, int s, int odd, int k) __attribute__((always_inline)) {
+            const int slot = s * C::kBlock + odd * C::kSlot;
             if (j < 4) {
-                f.b[s][j] = load16(slot + at_b + at[j]);
+                f.b[s][j] = load16(smem + at_b[j] + slot);
             } else if (j < 8) {
-                if (s < FM) f.a[s][j - 4] = load16(slot + at_a + at[j - 4]);
+                if (s < FM) f.a[s][j - 4] = load16(smem + at_a[j - 4] + slot);
             } else {
                 const int q = k >> 1, i = min(2 * k + h - min(4 * q, U - 4), 3);
-                const uint8_t *sc = smem + C::kScales + (q & 1) * 8192 + (32 * s + r32) * 16 + 4 * i;
+                const uint32_t at = (uint32_t)((q & 1) * C::kScaleSlot + 4 * i);
                 if (j == 8)
-                    f.sb[s] = *reinterpret_cast<const uint32_t *>(sc + (2 + wn) * 2048);
+                    f.sb[s] = *reinterpret_cast<const uint32_t *>(smem + at_sb + at + s * 512);
                 else if (s < FM)
-                    f.sa[s] = *reinterpret_cast<const uint32_t *>(sc + wm * 2048);
+                    f.sa[s] = *reinterpret_cast<const uint32_t *>(smem + at_sa + at + s * 512);
             }
         };
 
@@ -653,7 +672,7 @@ __global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int 
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int j = 0; j < kReads; ++j) read(x, j, s, 0);
+            for (int j = 0; j < kReads; ++j) read(x, j, s, 0, 0);
         lds_barrier();
 #pragma unroll
         for (int s = 0; s < 3; ++s) {
@@ -684,7 +703,7 @@ __global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int 
                                                                              acc[fn][f], kMxFormat, kMxFormat, S, cur.sb[fn], S, cur.sa[f]);
 #pragma unroll
                 for (int j = 0; j < kReads; ++j)
-                    if (j / kPer == b) read(nxt, j, S, k + 1);
+                    if (j / kPer == b) read(nxt, j, S, 1 - ODD, k + 1);
 #pragma unroll
                 for (int c = 0; c < kCopies; ++c)
                     if (c * kBlocks / kCopies == b) {
@@ -722,11 +741,12 @@ __global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int 
             place();
             prologue();
         }
+        const int sl = opaque_lane();
 #pragma unroll
         for (int f = 0; f < FM; ++f)
 #pragma unroll
             for (int fn = 0; fn < 4; ++fn)
-                mx_store_block<OUT>(g, acc[fn][f], tm0 + (wm * FM + f) * 32 + r32, tm1, tn0 + (wn * 4 + fn) * 32, h);
+                mx_store_block<OUT>(g, acc[fn][f], tm0 + (wm * FM + f) * 32 + (sl & 31), tm1, tn0 + (wn * 4 + fn) * 32, sl >> 5);
         const bool full = tm0 + 64 * FM <= tm1 && tn0 + 256 <= g.N;
         pending = full && g.N % 8 == 0 ? 4 * FM * (OUT == OUT_F32 ? 4 : 2) : 0;
     };
