@@ -202,31 +202,70 @@ __device__ __forceinline__ void mx_find_tile(const MxArgs &g, int v, int total, 
     m1 = min(end, m0 + 64 * fm);
 }
 
+// Eight or four neighbouring values of a row as OUT, from column n on; those
+// from N on are skipped.  Whole pieces go out in 16-byte (four of a 16-bit type:
+// 8-byte) stores whatever the row's alignment: global memory takes them at any
+// address of the element's alignment, and single stores of rows of odd length
+// cost more than the product (5314 x 845 x 1825: 30 us).
+template <int OUT>
+__device__ __forceinline__ void mx_store8(void *d, int64_t at, int n, int N, i32x4 packed)
+{
+    uint16_t *p = static_cast<uint16_t *>(d) + at + n;
+    if (n + 8 <= N) {
+        __builtin_memcpy(p, &packed, 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (n + i < N) p[i] = (uint16_t)((uint32_t)packed[i / 2] >> (16 * (i % 2)));
+    }
+}
+template <int OUT>
+__device__ __forceinline__ void mx_store4(void *d, int64_t at, int n, int N, float x0, float x1, float x2, float x3)
+{
+    if (OUT == OUT_F32) {
+        float *p = static_cast<float *>(d) + at + n;
+        const float x[4] = {x0, x1, x2, x3};
+        if (n + 4 <= N) {
+            __builtin_memcpy(p, x, 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                if (n + i < N) p[i] = x[i];
+        }
+    } else {
+        uint16_t *p = static_cast<uint16_t *>(d) + at + n;
+        const uint32_t w[2] = {mx_pack2<OUT>(x0, x1), mx_pack2<OUT>(x2, x3)};
+        if (n + 4 <= N) {
+            __builtin_memcpy(p, w, 8);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                if (n + i < N) p[i] = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
+        }
+    }
+}
+
 // One 32 x 32 block of D: row m, columns from nb; rows from m1 and columns from
-// N on are skipped.  bf16 and fp16 exchange halves where whole 16-byte stores
-// fit, so that a lane has eight neighbouring columns of its row.
+// N on are skipped.  bf16 and fp16 exchange halves, so that a lane has eight
+// neighbouring columns of its row.
 template <int OUT>
 __device__ __forceinline__ void mx_store_block(const MxArgs &g, const f32x16 &c, int m, int m1, int nb, int h)
 {
-    if (OUT != OUT_F32 && g.N % 8 == 0) {
+    const int64_t at = (int64_t)m * g.N;
+    if (OUT != OUT_F32) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const uint32_t x0 = mx_pack2<OUT>(c[8 * q + 0], c[8 * q + 1]), x1 = mx_pack2<OUT>(c[8 * q + 2], c[8 * q + 3]);
             const uint32_t y0 = mx_pack2<OUT>(c[8 * q + 4], c[8 * q + 5]), y1 = mx_pack2<OUT>(c[8 * q + 6], c[8 * q + 7]);
             const auto s0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
             const auto s1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
-            const int n = nb + 16 * q + 8 * h;
-            if (m < m1 && n < g.N)
-                *reinterpret_cast<i32x4 *>(static_cast<uint16_t *>(g.D) + (int64_t)m * g.N + n) =
-                    i32x4{(int32_t)s0[0], (int32_t)s1[0], (int32_t)s0[1], (int32_t)s1[1]};
+            if (m < m1)
+                mx_store8<OUT>(g.D, at, nb + 16 * q + 8 * h, g.N, i32x4{(int32_t)s0[0], (int32_t)s1[0], (int32_t)s0[1], (int32_t)s1[1]});
         }
     } else if (m < m1) {
-        Epilogue epi{g.D, nullptr, nullptr};
 #pragma unroll
-        for (int rg = 0; rg < 4; ++rg) {
-            const float x[4] = {c[4 * rg], c[4 * rg + 1], c[4 * rg + 2], c[4 * rg + 3]};
-            store_row4f<OUT>(epi, m, g.N, nb + 8 * rg + 4 * h, x);
-        }
+        for (int rg = 0; rg < 4; ++rg)
+            mx_store4<OUT>(g.D, at, nb + 8 * rg + 4 * h, g.N, c[4 * rg], c[4 * rg + 1], c[4 * rg + 2], c[4 * rg + 3]);
     }
 }
 
@@ -488,7 +527,7 @@ __global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(
         if (v >= total) break;
         // whole tiles issue one store per 16 bytes and lane; others count as none
         const bool full = tm0 + 64 * tfm <= tm1 && tn0 + T::BN <= g.N;
-        pending = full && g.N % 8 == 0 ? tfm * FN * (OUT == OUT_F32 ? 4 : 2) : 0;
+        pending = full ? tfm * FN * (OUT == OUT_F32 ? 4 : 2) : 0;
     }
 }
 
@@ -748,7 +787,7 @@ __global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int 
             for (int fn = 0; fn < 4; ++fn)
                 mx_store_block<OUT>(g, acc[fn][f], tm0 + (wm * FM + f) * 32 + (sl & 31), tm1, tn0 + (wn * 4 + fn) * 32, sl >> 5);
         const bool full = tm0 + 64 * FM <= tm1 && tn0 + 256 <= g.N;
-        pending = full && g.N % 8 == 0 ? 4 * FM * (OUT == OUT_F32 ? 4 : 2) : 0;
+        pending = full ? 4 * FM * (OUT == OUT_F32 ? 4 : 2) : 0;
     };
 
     while (v < total) {
@@ -1000,9 +1039,7 @@ __global__ __launch_bounds__(64 * kMxNarrowWaves) void gemm_mxfp4_narrow_kernel(
             const int e = GROUPED ? cur.strip / strips : 0;
             const int m = cur.m0 + 16 * f + r16;
             if (cur.m0 < 0 || m >= cur.m1) return;
-            Epilogue epi{g.D, nullptr, nullptr};
-            const float v[4] = {x.x, x.y, x.z, x.w};
-            store_row4f<OUT>(epi, m, g.N, 16 * (cur.strip - e * strips) + 4 * lg, v);
+            mx_store4<OUT>(g.D, (int64_t)m * g.N, 16 * (cur.strip - e * strips) + 4 * lg, g.N, x.x, x.y, x.z, x.w);
         };
         if (kw == 1) {
 #pragma unroll
