@@ -100,7 +100,8 @@ __device__ __forceinline__ void mx_dma16(i32x4 rsrc, uint32_t voffset, uint32_t 
 __device__ __forceinline__ void mx_dma16_at(i32x4 rsrc, uint32_t voffset, uint32_t soffset, uint32_t lds_base)
 {
     asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-                 : : "v"(voffset), "s"(rsrc), "s"(soffset), "s"(lds_base) : "memory", "m0");
+                 : : "v"(voffset), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(soffset)), "s"(__builtin_amdgcn_readfirstlane(lds_base))
+                 : "memory", "m0");
 }
 // mx_dma16 of data that is read once: it need not stay in the caches.
 __device__ __forceinline__ void mx_dma16_nt(i32x4 rsrc, uint32_t voffset, uint32_t lds_base)
@@ -279,26 +280,39 @@ __device__ __forceinline__ void mx_store_block(const MxArgs &g, const f32x16 &c,
 // MFMA picking byte s.  In LDS a row's eight 16-byte chunks are permuted by
 // c -> c ^ (row / 2) % 8: both the copies (8 rows of 128 bytes each) and the
 // fragment reads (16 rows of one chunk) touch all banks once.
+//
+// Scales come for two stages at a time, 16 bytes of every row: a copy of
+// scattered rows costs a cycle for each, whatever it brings (8192^3 lost 67 us
+// of 414 to copies of a dword).  The window is the row's last four units where
+// fewer are left; a scale past the row is then another of that row's: it meets
+// zero codes, and it is NaN only where the row's results are anyway.
+__device__ __forceinline__ int mx_scale_window(int q, int U) { return max(0, min(4 * q, U - 4)); }
+// Dword of a window that belongs to unit u.
+__device__ __forceinline__ int mx_scale_at(int u, int q, int U)
+{
+    const int first = mx_scale_window(q, U);
+    return min(u - first, min(3, U - 1 - first));
+}
+
 template <int FN>
 struct MxTile {
+    static_assert(FN == 1 || FN == 2, "64 or 128 columns");
     static constexpr int BN = 64 * FN;
-    static constexpr int NB = 2 * FN;                       // a wave's code copies of B per stage
-    static constexpr int NSB = FN >= 4 ? FN / 4 * 2 : 1;    // and its scale copies (32 rows each)
-    static constexpr int nsa(int fm) { return fm > 2 ? 2 : 1; }
-    static constexpr int per(int fm) { return NB + 2 * fm + NSB + nsa(fm); }
-    static constexpr int stage(int fm) { return (BN + 64 * fm) * 128 + (NSB + nsa(fm)) * 1024; }
-    // one workgroup per compute unit for the large tile, two for the others
-    static constexpr int kBudget = FN == 4 ? 158 * 1024 : 76 * 1024;
-    static constexpr int stages(int fm) { return kBudget / stage(fm) > 4 ? 4 : kBudget / stage(fm); }
-    static constexpr int ring(int fm) { return fm == 0 ? 0 : stages(fm) * stage(fm) > ring(fm - 1) ? stages(fm) * stage(fm) : ring(fm - 1); }
-    static constexpr int kRing = ring(FN);
-    static_assert(stages(FN) >= 2, "two stages at least");
+    static constexpr int kStages = FN == 1 ? 4 : 2;
+    static constexpr int NB = 2 * FN;                            // a wave's copies of B per stage
+    static constexpr int copies(int fm) { return NB + 2 * fm; }  // of codes; and one of scales in even stages
+    static constexpr int kCodes = 2 * BN * 128;                  // of a stage: B's rows, then A's
+    // scales of two stages: 1 KB a wave, of its 32 FN rows; two pairs are in flight, and the one being read
+    static constexpr int kPairs = kStages / 2 + 1, kScales = 4096;
+    static constexpr int kRing = kStages * kCodes + kPairs * kScales;
+    static constexpr int lds(int groups) { return kRing + 4 * (groups + 1 + 4); }
 };
 
 template <int FN, int OUT>
-__global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(MxArgs g, int tiles_n, int xcds)
+__global__ __launch_bounds__(256, 2) void gemm_mxfp4_tiled_kernel(MxArgs g, int tiles_n, int xcds)
 {
     using T = MxTile<FN>;
+    constexpr int ST = T::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     int32_t *cum = reinterpret_cast<int32_t *>(smem + T::kRing);  // [E + 1]: row tiles before group e
 
@@ -319,9 +333,10 @@ __global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(
         mx_find_tile<FN>(g, v, total, tiles_n, xcds, cum, e, m0, m1, n0, fm);
     };
 
-    // Source offsets of this lane in each copy of a stage.
-    i32x4 rsrc_a, rsrc_sa, rsrc_b, rsrc_sb;
-    uint32_t a_off[2 * FN], sa_off[2], b_off[T::NB], sb_off[T::NSB];
+    // Source offsets of this lane in each copy of a stage, and of its row in
+    // the copy of scales: waves 0, 1 serve A's rows, 32 FN each, waves 2, 3 B's.
+    i32x4 rsrc_a, rsrc_b, rsrc_s;
+    uint32_t a_off[2 * FN], b_off[T::NB], s_off;
     const int c8 = lane & 7;
     // chunk of the row's 128 bytes that goes to position c8 of row 8 p + lane / 8
     auto chunk = [&](int p) { return c8 ^ ((4 * p + (lane >> 4)) & 7); };
@@ -330,24 +345,15 @@ __global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(
         const int p = wave * T::NB + i;
         b_off[i] = (uint32_t)(8 * p + (lane >> 3)) * ldc + 16u * (uint32_t)chunk(p);
     }
-#pragma unroll
-    for (int i = 0; i < T::NSB; ++i) {
-        const int blk = wave * T::NSB + i;
-        sb_off[i] = 32 * blk < T::BN ? (uint32_t)(32 * blk + r32) * lds_ + 4u * (uint32_t)h : kOutOfRange;
-    }
     auto place = [&]() __attribute__((always_inline)) {  // resources and A's offsets of the current tile
         const int64_t brow = (int64_t)e * g.N + n0;
         const uint32_t nrows = (uint32_t)min(T::BN, g.N - n0);
+        const int64_t arow = g.rows == nullptr ? m0 : 0;
+        const uint32_t mrows = (uint32_t)(g.rows == nullptr ? m1 - m0 : g.T);
         rsrc_b = make_rsrc(g.B + brow * ldc, nrows * ldc);
-        rsrc_sb = make_rsrc(g.SFB + brow * lds_, nrows * lds_);
-        if (g.rows == nullptr) {
-            rsrc_a = make_rsrc(g.A + (int64_t)m0 * ldc, (uint32_t)(m1 - m0) * ldc);
-            rsrc_sa = make_rsrc(g.SFA + (int64_t)m0 * lds_, (uint32_t)(m1 - m0) * lds_);
-        } else {
-            rsrc_a = make_rsrc(g.A, (uint32_t)g.T * ldc);
-            rsrc_sa = make_rsrc(g.SFA, (uint32_t)g.T * lds_);
-        }
-        auto row_offset = [&](int r, uint32_t ld) __attribute__((always_inline)) -> uint32_t {  // of tile row r
+        rsrc_a = make_rsrc(g.A + arow * ldc, mrows * ldc);
+        rsrc_s = make_rsrc(wave < 2 ? g.SFA + arow * lds_ : g.SFB + brow * lds_, (wave < 2 ? mrows : nrows) * lds_);
+        auto row_offset = [&](int r, uint32_t ld) __attribute__((always_inline)) -> uint32_t {  // of tile row r of A
             if (g.rows == nullptr) return (uint32_t)r * ld;
             const int at = m0 + r < m1 ? g.rows[m0 + r] : -1;
             return at >= 0 && at < g.T ? (uint32_t)at * ld : kOutOfRange;
@@ -357,50 +363,55 @@ __global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(
             const int p = wave * 2 * fm + i;
             if (i < 2 * fm) a_off[i] = row_offset(8 * p + (lane >> 3), ldc) + 16u * (uint32_t)chunk(p);
         }
-        const int n = fm > 2 ? 2 : 1;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int blk = wave * n + i;
-            sa_off[i] = blk < 2 * fm ? row_offset(32 * blk + r32, lds_) + 4u * (uint32_t)h : kOutOfRange;
-        }
+        const int r = (wave & 1) * 32 * FN + lane;  // FN == 1: 32 rows, the upper lanes' zeros go nowhere
+        s_off = lane >= 32 * FN ? kOutOfRange : wave < 2 ? row_offset(r, lds_) : (uint32_t)r * lds_;
     };
 
-    // Copy j of stage kt's copies into the slot at `base`, for tiles of height
-    // 64 f.  Units past the row read zeros (zero codes: the scale beside them
-    // does not matter).
+    // Copy j of stage kt's copies into its slot, for tiles of height 64 f.
+    // Units past the row read zeros.
     auto issue = [&](int j, int f, int kt, uint32_t base) __attribute__((always_inline)) {
-        const uint32_t a0 = base + T::BN * 128, sb0 = a0 + (uint32_t)(64 * f) * 128, sa0 = sb0 + T::NSB * 1024;
-        const uint32_t koff = (uint32_t)kt * 128u, soff = (uint32_t)kt * 8u;
+        const uint32_t koff = (uint32_t)kt * 128u;
         if (j < T::NB) {
             const int p = wave * T::NB + j;
             const bool in = 2 * kt + (chunk(p) >> 2) < U;
-            mx_dma16(rsrc_b, in ? b_off[j] + koff : kOutOfRange, base + (uint32_t)p * 1024u);
-        } else if (j < T::NB + T::NSB) {
-            const int i = j - T::NB;
-            mx_dma4(rsrc_sb, 2 * kt + h < U ? sb_off[i] + soff : kOutOfRange, sb0 + (uint32_t)(wave * T::NSB + i) * 256u);
-        } else if (j < T::NB + T::NSB + 2 * f) {
-            const int i = j - T::NB - T::NSB, p = wave * 2 * f + i;
-            const bool in = 2 * kt + (chunk(p) >> 2) < U;
-            mx_dma16(rsrc_a, in ? a_off[i] + koff : kOutOfRange, a0 + (uint32_t)p * 1024u);
+            mx_dma16_at(rsrc_b, in ? b_off[j] : kOutOfRange, koff, base + (uint32_t)p * 1024u);
         } else {
-            const int i = j - T::NB - T::NSB - 2 * f, n = T::nsa(f);
-            mx_dma4(rsrc_sa, 2 * kt + h < U ? sa_off[i] + soff : kOutOfRange, sa0 + (uint32_t)(wave * n + i) * 256u);
+            const int i = j - T::NB, p = wave * 2 * f + i;
+            const bool in = 2 * kt + (chunk(p) >> 2) < U;
+            mx_dma16_at(rsrc_a, in ? a_off[i] : kOutOfRange, koff, base + T::BN * 128 + (uint32_t)p * 1024u);
         }
+    };
+    // The scales of stages 2 q and 2 q + 1.  Rows of fewer than four units have
+    // no window of 16 bytes: theirs are written by hand, and these copies bring
+    // zeros to a place that is not read.
+    auto issue_scales = [&](int q) __attribute__((always_inline)) {
+        const bool copied = U >= 4 && 4 * q < U;
+        mx_dma16_at(rsrc_s, copied ? s_off : kOutOfRange, (uint32_t)mx_scale_window(q, U) * 4u,
+                    lds0 + (uint32_t)(ST * T::kCodes + (U >= 4 ? q % T::kPairs : 1) * T::kScales) + (uint32_t)wave * 1024u);
     };
     // dispatch on the height; bodies see it as a constant
     auto with_height = [&](auto body) __attribute__((always_inline)) {
-        if (FN >= 4 && fm == 4) body(std::integral_constant<int, FN >= 4 ? 4 : 1>{});
-        else if (FN >= 4 && fm == 3) body(std::integral_constant<int, FN >= 4 ? 3 : 1>{});
-        else if (FN >= 2 && fm == 2) body(std::integral_constant<int, FN >= 2 ? 2 : 1>{});
+        if (FN >= 2 && fm == 2) body(std::integral_constant<int, FN >= 2 ? 2 : 1>{});
         else body(std::integral_constant<int, 1>{});
     };
     auto prologue = [&]() __attribute__((always_inline)) {
+        if (U < 4) {
+            const uint8_t *sf = wave < 2 ? g.SFA + (g.rows == nullptr ? (int64_t)m0 * lds_ : 0) : g.SFB + ((int64_t)e * g.N + n0) * lds_;
+            const uint32_t size = (wave < 2 ? (uint32_t)(g.rows == nullptr ? m1 - m0 : g.T) : (uint32_t)min(T::BN, g.N - n0)) * lds_;
+            for (int u = 0; u < 4; ++u) {
+                uint32_t x = 0;
+                if (u < U && s_off < size) x = *reinterpret_cast<const uint32_t *>(sf + s_off + 4 * u);
+                *reinterpret_cast<uint32_t *>(smem + ST * T::kCodes + wave * 1024 + lane * 16 + 4 * u) = x;
+            }
+        }
         with_height([&](auto height) __attribute__((always_inline)) {
             constexpr int FM = decltype(height)::value;
-#pragma nounroll
-            for (int st = 0; st < T::stages(FM); ++st)
 #pragma unroll
-                for (int j = 0; j < T::per(FM); ++j) issue(j, FM, st, lds0 + (uint32_t)(st * T::stage(FM)));
+            for (int st = 0; st < ST; ++st) {
+                if (st % 2 == 0) issue_scales(st / 2);
+#pragma unroll
+                for (int j = 0; j < T::copies(FM); ++j) issue(j, FM, st, lds0 + (uint32_t)(st * T::kCodes));
+            }
         });
     };
 
@@ -408,15 +419,16 @@ __global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(
     int pending = 0;     // store instructions of the previous tile, at least
     auto contract = [&](auto height) __attribute__((always_inline)) {
         constexpr int FM = decltype(height)::value;
-        constexpr int ST = T::stages(FM), PER = T::per(FM), STAGE = T::stage(FM);
-        constexpr uint32_t kA = T::BN * 128, kSB = kA + 64 * FM * 128, kSA = kSB + T::NSB * 1024;
+        constexpr int C = T::copies(FM);
+        constexpr uint32_t kA = T::BN * 128;
         constexpr int kBlocks = FM * FN, kReads = FM + FN;
-        if (pending >= 32)
-            wait_vmcnt<(ST - 1) * PER + 32>();
-        else if (pending >= 16)
-            wait_vmcnt<(ST - 1) * PER + 16>();
+        // copies younger than stage 0's; at a stage's end, than the next one's
+        constexpr int kFirst = (ST - 1) * C + (ST - 1) / 2, kSteady = (ST - 2) * C + (ST - 2) / 2;
+        constexpr int kStores = kBlocks * (OUT == OUT_F32 ? 4 : 2);
+        if (pending >= kStores)
+            wait_vmcnt<kFirst + kStores>();
         else
-            wait_vmcnt<(ST - 1) * PER>();
+            wait_vmcnt<kFirst>();
         lds_barrier();
 
 #pragma unroll
@@ -435,11 +447,19 @@ __global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(
             else
                 fa[s & 1][i - FN] = load16(base + kA + (wm * FM + i - FN) * 4096 + at);
         };
-        auto read_scale = [&](int i, const uint8_t *base) __attribute__((always_inline)) {
-            if (i < FN)
-                sb_next[i] = *reinterpret_cast<const uint32_t *>(base + kSB + (wn * FN + i) * 256 + 4 * lane);
-            else
-                sa_next[i - FN] = *reinterpret_cast<const uint32_t *>(base + kSA + (wm * FM + i - FN) * 256 + 4 * lane);
+        // row r of a half of FN blocks sits in that half's wave's kilobyte;
+        // A's rows are dealt out by FN blocks whatever the tile's height
+        auto read_scales = [&](int kt) __attribute__((always_inline)) {
+            const int q = kt >> 1, d = mx_scale_at(2 * kt + h, q, U);
+            const uint8_t *base = smem + ST * T::kCodes + (q % T::kPairs) * T::kScales + 4 * d;
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+                sb_next[i] = *reinterpret_cast<const uint32_t *>(base + (2 + wn) * 1024 + (32 * i + r32) * 16);
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const int blk = wm * FM + i;
+                sa_next[i] = *reinterpret_cast<const uint32_t *>(base + blk / FN * 1024 + (32 * (blk % FN) + r32) * 16);
+            }
         };
         auto take_scales = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -447,17 +467,17 @@ __global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(
 #pragma unroll
             for (int i = 0; i < FM; ++i) sa[i] = sa_next[i];
         };
+        read_scales(0);
 #pragma unroll
-        for (int i = 0; i < kReads; ++i) {
-            read_scale(i, smem);
-            read(0, i, smem);
-        }
+        for (int i = 0; i < kReads; ++i) read(0, i, smem);
         take_scales();
         // Step S: the next step's reads go out after the first MFMAs, the
         // copies that refill the stage's slot between all of the last step's.
         constexpr int kPer = (kReads + kBlocks - 1) / kBlocks;
         auto step = [&](auto index, const uint8_t *next, bool reads, bool refill, int kt, uint32_t slot_base) __attribute__((always_inline)) {
             constexpr int S = decltype(index)::value;
+            if (S == 3 && refill && (kt & 1) == 0) issue_scales((kt + ST) >> 1);
+            if (S == 3 && reads) read_scales(kt + 1);
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
                 const int fn = b / FM, f = b % FM;
@@ -465,13 +485,10 @@ __global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(
                                                                              acc[fn][f], kMxFormat, kMxFormat, S, sb[fn], S, sa[f]);
 #pragma unroll
                 for (int i = 0; i < kReads; ++i)
-                    if (reads && i / kPer == b) {
-                        read((S + 1) & 3, i, next);
-                        if (S == 3) read_scale(i, next);
-                    }
+                    if (reads && i / kPer == b) read((S + 1) & 3, i, next);
 #pragma unroll
-                for (int j = 0; j < PER; ++j)
-                    if (refill && j >= b * PER / kBlocks && j < (b + 1) * PER / kBlocks) issue(j, FM, kt + ST, slot_base);
+                for (int j = 0; j < C; ++j)
+                    if (refill && j >= b * C / kBlocks && j < (b + 1) * C / kBlocks) issue(j, FM, kt + ST, slot_base);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
@@ -481,19 +498,19 @@ __global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(
         using i3 = std::integral_constant<int, 3>;
         int slot = 0;
         for (int kt = 0; kt + 1 < ktiles; ++kt) {
-            const uint8_t *base = smem + slot * STAGE;
-            const uint32_t lbase = lds0 + (uint32_t)(slot * STAGE);
+            const uint8_t *base = smem + slot * T::kCodes;
+            const uint32_t lbase = lds0 + (uint32_t)(slot * T::kCodes);
             slot = slot + 1 == ST ? 0 : slot + 1;
-            const uint8_t *next = smem + slot * STAGE;
+            const uint8_t *next = smem + slot * T::kCodes;
             step(i0{}, base, true, false, kt, 0);
             step(i1{}, base, true, false, kt, 0);
             step(i2{}, base, true, false, kt, 0);
-            wait_vmcnt<(ST - 2) * PER>();
+            wait_vmcnt<kSteady>();
             lds_barrier();
             step(i3{}, next, true, true, kt, lbase);
             take_scales();
         }
-        const uint8_t *base = smem + slot * STAGE;
+        const uint8_t *base = smem + slot * T::kCodes;
         step(i0{}, base, true, false, 0, 0);
         step(i1{}, base, true, false, 0, 0);
         step(i2{}, base, true, false, 0, 0);
@@ -545,10 +562,7 @@ __global__ __launch_bounds__(256, FN == 4 ? 1 : 2) void gemm_mxfp4_tiled_kernel(
 // copies behind its last step, as the smaller tiles have them, the one wave of
 // a SIMD stood still for them: 8192^3 took 400 us.
 //
-// Scales come four units at a time: 16 bytes of every row for two stages, from
-// the row's last four units where fewer are left (U >= 4).  A scale past the
-// row is then another of that row's: it meets zero codes, and it is NaN only
-// where the row's results are anyway.
+// Scales as in the smaller tiles; U >= 4.
 struct MxLarge {
     // Codes: 32 KB for each half of A and of B, in it 8 KB for each block of 32
     // rows, 4 KB a slot (a read's slot and block fit its offset field);
@@ -640,7 +654,7 @@ __global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int 
     };
     auto copy_scales = [&](int i, int q) __attribute__((always_inline)) {
         const uint32_t o = 4 * q < U ? s_off[i] : kOutOfRange;
-        mx_dma16_at(rsrc_s, o, (uint32_t)min(4 * q, U - 4) * 4u, lds_scales + (uint32_t)((q & 1) * C::kScaleSlot + i * 1024));
+        mx_dma16_at(rsrc_s, o, (uint32_t)mx_scale_window(q, U) * 4u, lds_scales + (uint32_t)((q & 1) * C::kScaleSlot + i * 1024));
     };
     auto prologue = [&]() __attribute__((always_inline)) {
         copy_scales(0, 0);
@@ -691,7 +705,7 @@ __global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int 
             } else if (j < 8) {
                 if (s < FM) f.a[s][j - 4] = load16(smem + at_a[j - 4] + slot);
             } else {
-                const int q = k >> 1, i = min(2 * k + h - min(4 * q, U - 4), 3);
+                const int q = k >> 1, i = mx_scale_at(2 * k + h, q, U);
                 const uint32_t at = (uint32_t)((q & 1) * C::kScaleSlot + 4 * i);
                 if (j == 8)
                     f.sb[s] = *reinterpret_cast<const uint32_t *>(smem + at_sb + at + s * 512);

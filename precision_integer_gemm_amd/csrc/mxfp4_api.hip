@@ -95,14 +95,13 @@ lpgemm_status launch_tiled(const MxArgs &g, hipStream_t stream)
     static std::once_flag once[kMaxDevices];
     static hipError_t err[kMaxDevices];
     const auto kernel = &gemm_mxfp4_tiled_kernel<FN, OUT>;
-    constexpr int kLds = T::kRing + 4 * (LPGEMM_MXFP4_MAX_GROUPS + 1 + 4);
-    const lpgemm_status st = allow_lds(kernel, kLds, once, err);
+    const lpgemm_status st = allow_lds(kernel, T::lds(LPGEMM_MXFP4_MAX_GROUPS), once, err);
     if (st != LPGEMM_OK) return st;
     const int tiles_n = (int)ceil_div(g.N, 64 * FN);
     // at most one ragged row tile a group more than the rows fill
     const int64_t most = (ceil_div(g.R, 64 * FN) + (g.offsets ? std::min(g.E, g.R) : 0)) * tiles_n;
-    const unsigned blocks = (unsigned)std::min<int64_t>(most, (int64_t)compute_units() * (FN == 4 ? 1 : 2));
-    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), kLds, stream, g, tiles_n, kXcds);
+    const unsigned blocks = (unsigned)std::min<int64_t>(most, 2 * (int64_t)compute_units());
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), T::lds(g.E), stream, g, tiles_n, kXcds);
     return launched();
 }
 
@@ -206,7 +205,7 @@ lpgemm_status launch_product(const MxArgs &g, hipStream_t stream)
     // 32-bit row tile counts and offsets of a tile's rows
     if (ceil_div(g.R, tile) + g.E > INT32_MAX / ceil_div(g.N, tile)) return LPGEMM_ERR_UNSUPPORTED;
     if (tile == 256 && g.U >= MxLarge::kMinUnits) return launch_large<OUT>(g, stream);
-    return tile == 256 ? launch_tiled<4, OUT>(g, stream) : tile == 128 ? launch_tiled<2, OUT>(g, stream) : launch_tiled<1, OUT>(g, stream);
+    return tile >= 128 ? launch_tiled<2, OUT>(g, stream) : launch_tiled<1, OUT>(g, stream);
 }
 
 // Sizes and pointers that both products share; R rows of D.
