@@ -34,60 +34,6 @@ __device__ __forceinline__ void mx_group(const MxArgs &g, int e, int &begin, int
 
 __device__ __forceinline__ i32x8 mx_operand(i32x4 c) { return i32x8{c.x, c.y, c.z, c.w, 0, 0, 0, 0}; }
 
-// One wave per 32 x 32 block of D, operands straight from memory: lane l holds
-// row l % 32 of each operand and, of every 128-k unit, the two blocks
-// 2 (l / 32) and 2 (l / 32) + 1, one per MFMA.  B is the MFMA's row operand,
-// so a lane ends with four consecutive n of one m.
-template <int OUT>
-__global__ __launch_bounds__(256) void gemm_mxfp4_simple_kernel(MxArgs g)
-{
-    const int lane = threadIdx.x & 63;
-    const int r32 = lane & 31, h = lane >> 5;
-    const int e = blockIdx.z;
-    const int n0 = ((int)blockIdx.x * 4 + (int)(threadIdx.x >> 6)) * 32;
-    int begin, end;
-    mx_group(g, e, begin, end);
-    if (n0 >= g.N) return;
-    const int64_t brow = (int64_t)e * g.N + min(n0 + r32, g.N - 1);
-    const uint8_t *pb = g.B + brow * g.U * kMxUnitCodes + 32 * h;
-    const uint8_t *psb = g.SFB + brow * g.U * kMxUnitScales;
-    for (int m0 = begin + (int)blockIdx.y * 32; m0 < end; m0 += (int)gridDim.y * 32) {
-        const int m = m0 + r32;
-        int64_t arow = min(m, end - 1);
-        if (g.rows != nullptr) arow = g.rows[arow];
-        const bool live = arow >= 0 && arow < g.T;
-        if (!live) arow = 0;
-        const uint8_t *pa = g.A + arow * g.U * kMxUnitCodes + 32 * h;
-        const uint8_t *psa = g.SFA + arow * g.U * kMxUnitScales;
-        f32x16 acc = {};
-        for (int u = 0; u < g.U; ++u) {
-            uint32_t sa = *reinterpret_cast<const uint32_t *>(psa + u * 4) >> (16 * h);
-            const uint32_t sb = *reinterpret_cast<const uint32_t *>(psb + u * 4) >> (16 * h);
-            if (!live) sa = 0;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                i32x4 a = load16(pa + u * kMxUnitCodes + 16 * s);
-                if (!live) a = i32x4{0, 0, 0, 0};
-                const i32x4 b = load16(pb + u * kMxUnitCodes + 16 * s);
-                if (s == 0)
-                    acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(b), mx_operand(a), acc, kMxFormat,
-                                                                          kMxFormat, 0, sb, 0, sa);
-                else
-                    acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(b), mx_operand(a), acc, kMxFormat,
-                                                                          kMxFormat, 1, sb, 1, sa);
-            }
-        }
-        if (m < end) {
-            Epilogue epi{g.D, nullptr, nullptr};
-#pragma unroll
-            for (int rg = 0; rg < 4; ++rg) {
-                const float v[4] = {acc[4 * rg], acc[4 * rg + 1], acc[4 * rg + 2], acc[4 * rg + 3]};
-                store_row4f<OUT>(epi, m, g.N, n0 + 8 * rg + 4 * h, v);
-            }
-        }
-    }
-}
-
 // ---- tiled kernel ------------------------------------------------------------
 // 16 bytes (4 bytes) per lane from rsrc[voffset] into LDS at lds_base + 16 (4) lane;
 // offsets at or past the resource's size read zeros.
@@ -163,19 +109,67 @@ __device__ __forceinline__ int mx_tiles_before(const MxArgs &g, int high, int32_
     return __builtin_amdgcn_readfirstlane(cum[g.E]);
 }
 
-// The group that row tile rt belongs to: the last that begins at or before it.
-__device__ __forceinline__ int mx_group_of(int rt, int E, const int32_t *cum)
-{
-    const int lane = threadIdx.x & 63;
-    int n = 0;
-    for (int i = 0; i < E; i += 64) n += (int)__popcll(__ballot(i + lane < E && cum[i + lane] <= rt));
-    return __builtin_amdgcn_readfirstlane(n - 1);
-}
+// The groups' row tiles.  Up to 64 groups are held by the lanes of every wave
+// by itself, one load and a scan away (no barrier, nothing in LDS); more in
+// `cum`, whose bounds are read again where a tile needs them.
+struct MxGroups {
+    int begin = 0, end = 0, before = 0, total = 0;  // lane e: group e
+    const int32_t *cum = nullptr;
+
+    template <int WAVES>
+    __device__ __forceinline__ void init(const MxArgs &g, int high, int32_t *table)
+    {
+        const int lane = threadIdx.x & 63;
+        cum = table;
+        if (g.E > 64) {
+            total = mx_tiles_before<WAVES>(g, high, table);
+            return;
+        }
+        if (lane < g.E) mx_group(g, lane, begin, end);
+        const int own = (end - begin + high - 1) / high;
+        int run = own;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int o = __shfl_up(run, d);
+            if (lane >= d) run += o;
+        }
+        before = run - own;
+        total = __builtin_amdgcn_readlane(run, 63);
+    }
+    // The group that row tile rt belongs to, the last that begins at or before
+    // it: its rows [b, f) and the tiles before it.  `bounds`: begin | end << 16 in LDS.
+    __device__ __forceinline__ int of(const MxArgs &g, int rt, int &b, int &f, int &first, const uint32_t *bounds = nullptr) const
+    {
+        const int lane = threadIdx.x & 63;
+        int n = 0;
+        if (g.E > 64) {
+            for (int i = 0; i < g.E; i += 64) n += (int)__popcll(__ballot(i + lane < g.E && cum[i + lane] <= rt));
+            const int e = __builtin_amdgcn_readfirstlane(n - 1);
+            first = __builtin_amdgcn_readfirstlane(cum[e]);
+            if (bounds != nullptr) {
+                const uint32_t bound = __builtin_amdgcn_readfirstlane(bounds[e]);
+                b = (int)(bound & 0xFFFFu);
+                f = (int)(bound >> 16);
+            } else {
+                mx_group(g, e, b, f);
+                b = __builtin_amdgcn_readfirstlane(b);
+                f = __builtin_amdgcn_readfirstlane(f);
+            }
+            return e;
+        }
+        n = (int)__popcll(__ballot(lane < g.E && before <= rt));
+        const int e = __builtin_amdgcn_readfirstlane(n - 1);
+        first = __builtin_amdgcn_readlane(before, e);
+        b = __builtin_amdgcn_readlane(begin, e);
+        f = __builtin_amdgcn_readlane(end, e);
+        return e;
+    }
+};
 
 // Tile v of `total`: group e, rows [m0, m1) of D, height 64 fm, columns from
-// n0, for tiles of up to 64 FN rows and 64 FN columns.
-template <int FN>
-__device__ __forceinline__ void mx_find_tile(const MxArgs &g, int v, int total, int tiles_n, int xcds, const int32_t *cum, int &e,
+// n0, for tiles of up to 64 HM rows and 64 FN columns.
+template <int HM, int FN>
+__device__ __forceinline__ void mx_find_tile(const MxArgs &g, int v, int total, int tiles_n, int xcds, const MxGroups &groups, int &e,
                                              int &m0, int &m1, int &n0, int &fm)
 {
     // XCD-contiguous: workgroups v, v + 8, .. share an L2 and take neighbouring tiles
@@ -183,14 +177,8 @@ __device__ __forceinline__ void mx_find_tile(const MxArgs &g, int v, int total, 
     const int id = v < whole ? (v % xcds) * (whole / xcds) + v / xcds : v;
     int begin = 0, end = g.R, first = 0;
     e = 0;
-    if (g.offsets != nullptr) {
-        e = mx_group_of(id / tiles_n, g.E, cum);
-        first = __builtin_amdgcn_readfirstlane(cum[e]);
-        mx_group(g, e, begin, end);
-    }
-    begin = __builtin_amdgcn_readfirstlane(begin);
-    end = __builtin_amdgcn_readfirstlane(end);
-    const int blocks = (end - begin + 63) / 64, c = (blocks + FN - 1) / FN;  // of 64 rows; tiles
+    if (g.offsets != nullptr) e = groups.of(g, id / tiles_n, begin, end, first);
+    const int blocks = (end - begin + 63) / 64, c = (blocks + HM - 1) / HM;  // of 64 rows; tiles
     // bands of four row tiles, the band's tiles of one column together
     const int in_group = id - first * tiles_n;
     const int band = in_group / (4 * tiles_n), high = min(4, c - 4 * band);
@@ -270,6 +258,55 @@ __device__ __forceinline__ void mx_store_block(const MxArgs &g, const f32x16 &c,
     }
 }
 
+// 32 rows x 32 W columns of D, blocks c(0) .. c(W - 1) side by side, through the
+// wave's own `stage` of LDS (mx_stage_bytes), so that a store instruction writes
+// whole rows of them.  In the MFMA's layout it writes 32 bytes of each of 32
+// rows, which memory takes far more slowly: 2848 x 2880 fp32 went out at 2 TB/s.
+template <int OUT, int W>
+__host__ __device__ constexpr int mx_stage_pitch() { return 32 * W * (OUT == OUT_F32 ? 4 : 2) + 16; }
+template <int OUT, int W>
+__host__ __device__ constexpr int mx_stage_bytes() { return 32 * mx_stage_pitch<OUT, W>(); }
+template <int OUT, int W, typename Block>
+__device__ __forceinline__ void mx_store_rows(const MxArgs &g, uint8_t *stage, Block c, int m0, int m1, int nb)
+{
+    constexpr int kPitch = mx_stage_pitch<OUT, W>();
+    int lane = (int)threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));  // addresses are computed here, not kept through the K loop
+    uint8_t *mine = stage + (lane & 31) * kPitch;
+    const int h = lane >> 5;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const f32x16 &x = c(w);
+#pragma unroll
+        for (int rg = 0; rg < 4; ++rg) {
+            const int col = 32 * w + 8 * rg + 4 * h;
+            if (OUT == OUT_F32) {
+                const i32x4 v = {(int32_t)__float_as_uint(x[4 * rg]), (int32_t)__float_as_uint(x[4 * rg + 1]),
+                                 (int32_t)__float_as_uint(x[4 * rg + 2]), (int32_t)__float_as_uint(x[4 * rg + 3])};
+                *reinterpret_cast<i32x4 *>(mine + 4 * col) = v;
+            } else {
+                *reinterpret_cast<uint64_t *>(mine + 2 * col) =
+                    (uint64_t)mx_pack2<OUT>(x[4 * rg + 2], x[4 * rg + 3]) << 32 | mx_pack2<OUT>(x[4 * rg], x[4 * rg + 1]);
+            }
+        }
+    }
+    // the wave's own writes, read by its other lanes
+    __builtin_amdgcn_wave_barrier();
+    constexpr int kPiece = OUT == OUT_F32 ? 4 : 8, kLanes = 32 * W / kPiece, kRows = 64 / kLanes;  // columns a lane; lanes a row; rows at a time
+    const int sub = lane / kLanes, n = nb + lane % kLanes * kPiece;
+#pragma unroll
+    for (int i = 0; i < 32 / kRows; ++i) {
+        const int row = i * kRows + sub, m = m0 + row;
+        const i32x4 v = *reinterpret_cast<const i32x4 *>(stage + row * kPitch + lane % kLanes * 16);
+        if (m >= m1) continue;
+        if (OUT == OUT_F32)
+            mx_store4<OUT>(g.D, (int64_t)m * g.N, n, g.N, __int_as_float(v[0]), __int_as_float(v[1]), __int_as_float(v[2]), __int_as_float(v[3]));
+        else
+            mx_store8<OUT>(g.D, (int64_t)m * g.N, n, g.N, v);
+    }
+    __builtin_amdgcn_wave_barrier();
+}
+
 // A workgroup of four waves (2 x 2) computes tiles of 64 FM x 64 FN, FM = 1 ..
 // FN chosen tile by tile from its group's rows, so a group wastes less than 64
 // rows whatever its size; a wave holds FM x FN blocks of 32 x 32.
@@ -294,24 +331,25 @@ __device__ __forceinline__ int mx_scale_at(int u, int q, int U)
     return min(u - first, min(3, U - 1 - first));
 }
 
-template <int FN>
+template <int HM, int FN, int STAGES>
 struct MxTile {
-    static_assert(FN == 1 || FN == 2, "64 or 128 columns");
+    static_assert((FN == 1 || FN == 2) && HM <= FN && (STAGES == 2 || STAGES == 4), "heights up to HM, 64 or 128 columns");
     static constexpr int BN = 64 * FN;
-    static constexpr int kStages = FN == 1 ? 4 : 2;
+    static constexpr int kStages = STAGES;
     static constexpr int NB = 2 * FN;                            // a wave's copies of B per stage
     static constexpr int copies(int fm) { return NB + 2 * fm; }  // of codes; and one of scales in even stages
-    static constexpr int kCodes = 2 * BN * 128;                  // of a stage: B's rows, then A's
+    static constexpr int kCodes = (BN + 64 * HM) * 128;          // of a stage: B's rows, then A's
     // scales of two stages: 1 KB a wave, of its 32 FN rows; two pairs are in flight, and the one being read
     static constexpr int kPairs = kStages / 2 + 1, kScales = 4096;
     static constexpr int kRing = kStages * kCodes + kPairs * kScales;
     static constexpr int lds(int groups) { return kRing + 4 * (groups + 1 + 4); }
 };
 
-template <int FN, int OUT>
+template <int HM, int FN, int STAGES, int OUT>
 __global__ __launch_bounds__(256, 2) void gemm_mxfp4_tiled_kernel(MxArgs g, int tiles_n, int xcds)
 {
-    using T = MxTile<FN>;
+    using T = MxTile<HM, FN, STAGES>;
+    static_assert(4 * mx_stage_bytes<OUT, FN>() <= T::kStages * T::kCodes, "the ring holds the rows on their way out");
     constexpr int ST = T::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     int32_t *cum = reinterpret_cast<int32_t *>(smem + T::kRing);  // [E + 1]: row tiles before group e
@@ -324,19 +362,20 @@ __global__ __launch_bounds__(256, 2) void gemm_mxfp4_tiled_kernel(MxArgs g, int 
     const uint32_t ldc = (uint32_t)U * kMxUnitCodes, lds_ = (uint32_t)U * kMxUnitScales;
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(smem);
 
-    const int total_rt = g.offsets == nullptr ? (g.R + 64 * FN - 1) / (64 * FN) : mx_tiles_before<4>(g, 64 * FN, cum);
-    const int total = total_rt * tiles_n;
+    MxGroups groups;
+    if (g.offsets != nullptr) groups.init<4>(g, 64 * HM, cum);
+    const int total = (g.offsets == nullptr ? (g.R + 64 * HM - 1) / (64 * HM) : groups.total) * tiles_n;
 
     // The current tile: group e, rows [m0, m1) of D, columns from n0, height 64 fm.
     int e = 0, m0 = 0, m1 = 0, n0 = 0, fm = 0;
     auto find = [&](int v) __attribute__((always_inline)) {
-        mx_find_tile<FN>(g, v, total, tiles_n, xcds, cum, e, m0, m1, n0, fm);
+        mx_find_tile<HM, FN>(g, v, total, tiles_n, xcds, groups, e, m0, m1, n0, fm);
     };
 
     // Source offsets of this lane in each copy of a stage, and of its row in
     // the copy of scales: waves 0, 1 serve A's rows, 32 FN each, waves 2, 3 B's.
     i32x4 rsrc_a, rsrc_b, rsrc_s;
-    uint32_t a_off[2 * FN], b_off[T::NB], s_off;
+    uint32_t a_off[2 * HM], b_off[T::NB], s_off;
     const int c8 = lane & 7;
     // chunk of the row's 128 bytes that goes to position c8 of row 8 p + lane / 8
     auto chunk = [&](int p) { return c8 ^ ((4 * p + (lane >> 4)) & 7); };
@@ -359,7 +398,7 @@ __global__ __launch_bounds__(256, 2) void gemm_mxfp4_tiled_kernel(MxArgs g, int 
             return at >= 0 && at < g.T ? (uint32_t)at * ld : kOutOfRange;
         };
 #pragma unroll
-        for (int i = 0; i < 2 * FN; ++i) {
+        for (int i = 0; i < 2 * HM; ++i) {
             const int p = wave * 2 * fm + i;
             if (i < 2 * fm) a_off[i] = row_offset(8 * p + (lane >> 3), ldc) + 16u * (uint32_t)chunk(p);
         }
@@ -391,7 +430,7 @@ __global__ __launch_bounds__(256, 2) void gemm_mxfp4_tiled_kernel(MxArgs g, int 
     };
     // dispatch on the height; bodies see it as a constant
     auto with_height = [&](auto body) __attribute__((always_inline)) {
-        if (FN >= 2 && fm == 2) body(std::integral_constant<int, FN >= 2 ? 2 : 1>{});
+        if (HM >= 2 && fm == 2) body(std::integral_constant<int, HM >= 2 ? 2 : 1>{});
         else body(std::integral_constant<int, 1>{});
     };
     auto prologue = [&]() __attribute__((always_inline)) {
@@ -415,8 +454,7 @@ __global__ __launch_bounds__(256, 2) void gemm_mxfp4_tiled_kernel(MxArgs g, int 
         });
     };
 
-    f32x16 acc[FN][FN];  // [n block][m block]
-    int pending = 0;     // store instructions of the previous tile, at least
+    f32x16 acc[FN][HM];  // [n block][m block]
     auto contract = [&](auto height) __attribute__((always_inline)) {
         constexpr int FM = decltype(height)::value;
         constexpr int C = T::copies(FM);
@@ -424,11 +462,7 @@ __global__ __launch_bounds__(256, 2) void gemm_mxfp4_tiled_kernel(MxArgs g, int 
         constexpr int kBlocks = FM * FN, kReads = FM + FN;
         // copies younger than stage 0's; at a stage's end, than the next one's
         constexpr int kFirst = (ST - 1) * C + (ST - 1) / 2, kSteady = (ST - 2) * C + (ST - 2) / 2;
-        constexpr int kStores = kBlocks * (OUT == OUT_F32 ? 4 : 2);
-        if (pending >= kStores)
-            wait_vmcnt<kFirst + kStores>();
-        else
-            wait_vmcnt<kFirst>();
+        wait_vmcnt<kFirst>();
         lds_barrier();
 
 #pragma unroll
@@ -518,33 +552,20 @@ __global__ __launch_bounds__(256, 2) void gemm_mxfp4_tiled_kernel(MxArgs g, int 
         wait_vmcnt<0>();  // copies past the last stage
     };
 
-    int v = blockIdx.x;
-    if (v >= total) return;
-    find(v);
-    place();
-    prologue();
-    for (;;) {
+    for (int v = blockIdx.x; v < total; v += (int)gridDim.x) {
+        find(v);
+        place();
+        prologue();
         with_height(contract);
-
-        const int tm0 = m0, tm1 = m1, tn0 = n0, tfm = fm;
-        v += (int)gridDim.x;
         lds_barrier();  // every wave is done with the ring
-        if (v < total) {
-            find(v);
-            place();
-            prologue();
-        }
+        uint8_t *out_stage = smem + wave * mx_stage_bytes<OUT, FN>();
 #pragma unroll
-        for (int f = 0; f < FN; ++f) {
-            if (f >= tfm) break;
-#pragma unroll
-            for (int fn = 0; fn < FN; ++fn)
-                mx_store_block<OUT>(g, acc[fn][f], tm0 + (wm * tfm + f) * 32 + r32, tm1, tn0 + (wn * FN + fn) * 32, h);
+        for (int f = 0; f < HM; ++f) {
+            if (f >= fm) break;
+            mx_store_rows<OUT, FN>(g, out_stage, [&](int w) -> const f32x16 & { return acc[w][f]; }, m0 + (wm * fm + f) * 32, m1,
+                                   n0 + wn * FN * 32);
         }
-        if (v >= total) break;
-        // whole tiles issue one store per 16 bytes and lane; others count as none
-        const bool full = tm0 + 64 * tfm <= tm1 && tn0 + T::BN <= g.N;
-        pending = full ? tfm * FN * (OUT == OUT_F32 ? 4 : 2) : 0;
+        lds_barrier();  // every wave's rows have left it
     }
 }
 
@@ -597,13 +618,14 @@ __global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int 
     const uint32_t ldc = (uint32_t)U * kMxUnitCodes, lds_ = (uint32_t)U * kMxUnitScales;
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(smem);
 
-    const int total_rt = g.offsets == nullptr ? (g.R + 255) / 256 : mx_tiles_before<4>(g, 256, cum);
-    const int total = total_rt * tiles_n;
+    MxGroups groups;
+    if (g.offsets != nullptr) groups.init<4>(g, 256, cum);
+    const int total = (g.offsets == nullptr ? (g.R + 255) / 256 : groups.total) * tiles_n;
 
     // The current tile: group e, rows [m0, m1) of D, columns from n0, height 64 fm.
     int e = 0, m0 = 0, m1 = 0, n0 = 0, fm = 0;
     auto find = [&](int v) __attribute__((always_inline)) {
-        mx_find_tile<4>(g, v, total, tiles_n, xcds, cum, e, m0, m1, n0, fm);
+        mx_find_tile<4, 4>(g, v, total, tiles_n, xcds, groups, e, m0, m1, n0, fm);
     };
 
     // This wave's copies: half `wave % 2` of A (waves 0, 1) or B.
@@ -793,6 +815,16 @@ __global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int 
             find(v);
             place();
             prologue();
+        } else if (OUT != OUT_F32) {
+            // no copies follow: the ring is free for whole rows (fp32 values, in
+            // both branches unchanged, would be taken out of the accumulators
+            // ahead of the branch and spilled)
+            uint8_t *out_stage = smem + wave * mx_stage_bytes<OUT, 4>();
+#pragma unroll
+            for (int f = 0; f < FM; ++f)
+                mx_store_rows<OUT, 4>(g, out_stage, [&](int w) -> const f32x16 & { return acc[w][f]; }, tm0 + (wm * FM + f) * 32, tm1,
+                                      tn0 + wn * 128);
+            return;
         }
         const int sl = opaque_lane();
 #pragma unroll
@@ -869,15 +901,19 @@ __global__ __launch_bounds__(64 * kMxNarrowWaves) void gemm_mxfp4_narrow_kernel(
     const uint8_t *mine = smem + ring;
 
     int items = strips;
+    MxGroups groups;
     if (GROUPED) {
         if (g.rows != nullptr)
             for (int i = threadIdx.x; i < g.R; i += 64 * kMxNarrowWaves) index[i] = g.rows[i];
-        for (int i = threadIdx.x; i < g.E; i += 64 * kMxNarrowWaves) {
-            int begin, end;
-            mx_group(g, i, begin, end);
-            bounds[i] = (uint32_t)begin | (uint32_t)end << 16;
-        }
-        items = mx_tiles_before<kMxNarrowWaves>(g, 16, cum) * strips;  // also the barrier behind the indices
+        if (g.E > 64)
+            for (int i = threadIdx.x; i < g.E; i += 64 * kMxNarrowWaves) {
+                int begin, end;
+                mx_group(g, i, begin, end);
+                bounds[i] = (uint32_t)begin | (uint32_t)end << 16;
+            }
+        groups.init<kMxNarrowWaves>(g, 16, cum);
+        items = groups.total * strips;
+        __syncthreads();  // the indices
     }
     const int rounds = (items - (int)blockIdx.x * side_by_side + (int)gridDim.x * side_by_side - 1) / ((int)gridDim.x * side_by_side);
     if (rounds <= 0) return;
@@ -903,10 +939,8 @@ __global__ __launch_bounds__(64 * kMxNarrowWaves) void gemm_mxfp4_narrow_kernel(
         it.m1 = g.R;
         it.strip = id;
         if (GROUPED && id < items) {
-            const int e = mx_group_of(id / strips, g.E, cum);
-            const int first = __builtin_amdgcn_readfirstlane(cum[e]);
-            const uint32_t bound = __builtin_amdgcn_readfirstlane(bounds[e]);
-            const int begin = (int)(bound & 0xFFFFu), end = (int)(bound >> 16);
+            int begin, end, first;
+            const int e = groups.of(g, id / strips, begin, end, first, bounds);
             const int tiles = (end - begin + 15) / 16, in_group = id - first * strips;
             // a strip's row tiles one after another: its later reads come from the caches
             it.strip = e * strips + in_group / tiles;

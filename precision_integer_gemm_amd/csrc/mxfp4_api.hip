@@ -88,19 +88,19 @@ lpgemm_status allow_lds(Kernel kernel, int bytes, std::once_flag *once, hipError
     return err[dev] == hipSuccess ? LPGEMM_OK : LPGEMM_ERR_HIP;
 }
 
-template <int FN, int OUT>
+template <int HM, int FN, int STAGES, int OUT>
 lpgemm_status launch_tiled(const MxArgs &g, hipStream_t stream)
 {
-    using T = MxTile<FN>;
+    using T = MxTile<HM, FN, STAGES>;
     static std::once_flag once[kMaxDevices];
     static hipError_t err[kMaxDevices];
-    const auto kernel = &gemm_mxfp4_tiled_kernel<FN, OUT>;
+    const auto kernel = &gemm_mxfp4_tiled_kernel<HM, FN, STAGES, OUT>;
     const lpgemm_status st = allow_lds(kernel, T::lds(LPGEMM_MXFP4_MAX_GROUPS), once, err);
     if (st != LPGEMM_OK) return st;
     const int tiles_n = (int)ceil_div(g.N, 64 * FN);
     // at most one ragged row tile a group more than the rows fill
-    const int64_t most = (ceil_div(g.R, 64 * FN) + (g.offsets ? std::min(g.E, g.R) : 0)) * tiles_n;
-    const unsigned blocks = (unsigned)std::min<int64_t>(most, 2 * (int64_t)compute_units());
+    const int64_t most = (ceil_div(g.R, 64 * HM) + (g.offsets ? std::min(g.E, g.R) : 0)) * tiles_n;
+    const unsigned blocks = (unsigned)std::min<int64_t>(most, (T::lds(g.E) > 80 * 1024 ? 1 : 2) * (int64_t)compute_units());
     hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), T::lds(g.E), stream, g, tiles_n, kXcds);
     return launched();
 }
@@ -117,14 +117,6 @@ lpgemm_status launch_large(const MxArgs &g, hipStream_t stream)
     const int64_t most = (ceil_div(g.R, 256) + (g.offsets ? std::min(g.E, g.R) : 0)) * tiles_n;
     hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(most, compute_units())), dim3(256), MxLarge::lds(g.E), stream, g, tiles_n,
                        kXcds);
-    return launched();
-}
-
-template <int OUT>
-lpgemm_status launch_simple(const MxArgs &g, hipStream_t stream)
-{
-    const dim3 grid((unsigned)ceil_div(g.N, 128), (unsigned)std::min<int64_t>(ceil_div(g.R, 32), 65535), (unsigned)g.E);
-    hipLaunchKernelGGL((gemm_mxfp4_simple_kernel<OUT>), grid, dim3(256), 0, stream, g);
     return launched();
 }
 
@@ -183,29 +175,80 @@ lpgemm_status launch_narrow_any(const MxArgs &g, hipStream_t stream)
                          : launch_narrow<2, 4, false, OUT>(g, kw, 4, stream);
 }
 
+// The tiled kernels' shapes and what one of their tiles costs in time: us for
+// a stage (256 k) at heights of 64, 128, 192 and 256 rows, and for a tile.  A
+// compute unit draws about 60 GB/s of codes from beyond its XCD's L2 and 100
+// from it, so small tiles pay for their copies and large ones, one to a
+// compute unit, for a tile's beginning and end.  Fitted on MI355X; where they
+// meet (us, 64 x 64 / 64 x 128 / 128 x 128 / 128 x 128 with four stages / 256 x 256):
+//     1024 x 1024 x 4096     8.5 /  9.8 / 12.6 / 13.1 /  26
+//     513 x 6086 x 384       9.2 /  6.3 /  6.7 /  7.4 /   -
+//     199 x 8582 x 6277       23 /   22 /   23 /   19 /  40
+//     2848 x 2880 x 3200      41 /   39 /   34 /   36 /  31
+//     4096 x 4096 x 4096      88 /    - /   50 /    - /  41
+struct Shape {
+    int high, wide, stages;
+    double stage[4], tile;
+};
+constexpr Shape kShapes[] = {{64, 64, 4, {0.25}, 1.2},
+                             {64, 128, 2, {0.42}, 1.1},
+                             {128, 128, 2, {0.42, 0.58}, 1.5},
+                             {128, 128, 4, {0.50, 0.62}, 2.0},
+                             {256, 256, 2, {0.80, 1.10, 1.45, 1.75}, 11.0}};
+enum { kShape64, kShape64x128, kShape128, kShape128Deep, kShape256, kShapeCount };
+
+// The shape that should take the least time for R rows in `groups` equal groups.
+int choose_shape(const MxArgs &g, int64_t cu)
+{
+    const int64_t groups = g.offsets ? std::min(g.E, g.R) : 1, rows = ceil_div(g.R, groups), stages = ceil_div(g.U, 2);
+    int best = kShape64;
+    double least = 0;
+    for (int i = 0; i < kShapeCount; ++i) {
+        const Shape &s = kShapes[i];
+        if (i == kShape256 && g.U < MxLarge::kMinUnits) continue;
+        const int64_t c = ceil_div(rows, s.high), blocks = ceil_div(ceil_div(rows, 64), c);  // tiles of a group, their height / 64
+        const int64_t tiles = groups * c * ceil_div(g.N, s.wide);
+        if (i == kShape128Deep && tiles > cu) continue;  // one to a compute unit
+        const double t = (double)ceil_div(tiles, cu) * ((double)stages * s.stage[blocks - 1] + s.tile);
+        if (i == 0 || t < least) {
+            best = i;
+            least = t;
+        }
+    }
+    return best;
+}
+
+template <int OUT>
+lpgemm_status launch_shape(const MxArgs &g, int shape, hipStream_t stream)
+{
+    // 32-bit tile counts
+    const Shape &s = kShapes[shape];
+    if (ceil_div(g.R, s.high) + g.E > INT32_MAX / ceil_div(g.N, s.wide)) return LPGEMM_ERR_UNSUPPORTED;
+    switch (shape) {
+    case kShape64: return launch_tiled<1, 1, 4, OUT>(g, stream);
+    case kShape64x128: return launch_tiled<1, 2, 2, OUT>(g, stream);
+    case kShape128: return launch_tiled<2, 2, 2, OUT>(g, stream);
+    case kShape128Deep: return launch_tiled<2, 2, 4, OUT>(g, stream);
+    default: return g.U >= MxLarge::kMinUnits ? launch_large<OUT>(g, stream) : launch_tiled<2, 2, 2, OUT>(g, stream);
+    }
+}
+
 template <int OUT>
 lpgemm_status launch_product(const MxArgs &g, hipStream_t stream)
 {
     const int64_t cu = compute_units();
-    auto tiles = [&](int64_t edge) { return (ceil_div(g.R, edge) + (g.offsets ? g.E / 2 : 0)) * ceil_div(g.N, edge); };
-    int tile = 4 * tiles(256) >= 3 * cu ? 256 : tiles(128) >= cu ? 128 : 64;
     switch (forced_kernel()) {
     case LPGEMM_KERNEL_AUTO:
         // grouped: up to eight rows a group on average
         if (narrow_serves(g) && (g.offsets == nullptr || g.R <= 8 * (int64_t)g.E)) return launch_narrow_any<OUT>(g, stream);
-        break;
-    case LPGEMM_KERNEL_TILED: break;
-    case LPGEMM_KERNEL_GENERAL: return launch_simple<OUT>(g, stream);
-    case LPGEMM_KERNEL_TILED_64: tile = 64; break;
-    case LPGEMM_KERNEL_TILED_128: tile = 128; break;
-    case LPGEMM_KERNEL_TILED_256: tile = 256; break;
+        return launch_shape<OUT>(g, choose_shape(g, cu), stream);
+    case LPGEMM_KERNEL_TILED: return launch_shape<OUT>(g, choose_shape(g, cu), stream);
+    case LPGEMM_KERNEL_TILED_64: return launch_shape<OUT>(g, kShape64, stream);
+    case LPGEMM_KERNEL_TILED_128: return launch_shape<OUT>(g, g.R * (int64_t)g.N > 128 * 128 * cu ? kShape128 : kShape128Deep, stream);
+    case LPGEMM_KERNEL_TILED_256: return launch_shape<OUT>(g, kShape256, stream);
     case LPGEMM_KERNEL_SKINNY: return narrow_serves(g) ? launch_narrow_any<OUT>(g, stream) : LPGEMM_ERR_UNSUPPORTED;
     default: return LPGEMM_ERR_UNSUPPORTED;
     }
-    // 32-bit row tile counts and offsets of a tile's rows
-    if (ceil_div(g.R, tile) + g.E > INT32_MAX / ceil_div(g.N, tile)) return LPGEMM_ERR_UNSUPPORTED;
-    if (tile == 256 && g.U >= MxLarge::kMinUnits) return launch_large<OUT>(g, stream);
-    return tile >= 128 ? launch_tiled<2, OUT>(g, stream) : launch_tiled<1, OUT>(g, stream);
 }
 
 // Sizes and pointers that both products share; R rows of D.
