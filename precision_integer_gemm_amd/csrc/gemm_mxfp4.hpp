@@ -857,7 +857,8 @@ __global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int 
 // touch all banks once.  The KW partial tiles are added in LDS in a fixed
 // order, by the subgroup's waves in turn.
 //
-// A stays in registers (product: 16 FA rows, S stages a wave) or, where it
+// A stays in registers (product: 16 FA rows, S stages a wave; more rows are
+// the grid's second dimension, each tile reading B for itself) or, where it
 // changes from strip to strip (grouped: tiles of up to 16 rows of one group,
 // gathered), comes through the ring beside B.
 constexpr int kMxNarrowWaves = 8;
@@ -884,6 +885,13 @@ __global__ __launch_bounds__(64 * kMxNarrowWaves) void gemm_mxfp4_narrow_kernel(
 {
     static_assert(!GROUPED || (FA == 1 && S == 1), "grouped: one row tile, stages counted at run time");
     using C = MxNarrow<GROUPED>;
+    if (!GROUPED) {  // a workgroup's row tile, as a product of its own
+        const int m0 = (int)blockIdx.y * 16 * FA;
+        g.A += (int64_t)m0 * g.U * kMxUnitCodes;
+        g.SFA += (int64_t)m0 * g.U * kMxUnitScales;
+        g.D = static_cast<uint8_t *>(g.D) + (int64_t)m0 * g.N * (OUT == OUT_F32 ? 4 : 2);
+        g.R = min(g.R - m0, 16 * FA);
+    }
     extern __shared__ __align__(1024) uint8_t smem[];
     mx_f32x4 *sums = reinterpret_cast<mx_f32x4 *>(smem + C::kRing);  // [2][waves][64]
     int32_t *cum = reinterpret_cast<int32_t *>(smem + C::kRing + C::kSums);

@@ -130,41 +130,54 @@ lpgemm_status launch_narrow(const MxArgs &g, int kw, int stages, hipStream_t str
     const lpgemm_status st = allow_lds(kernel, C::lds(kMxNarrowGroups), once, err);
     if (st != LPGEMM_OK) return st;
     const int64_t items = ceil_div(g.N, 16) * (GROUPED ? ceil_div(g.R, 16) + std::min(g.E, g.R) : 1);
-    const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(items, kMxNarrowWaves / kw), compute_units());
-    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(64 * kMxNarrowWaves), C::lds(g.E), stream, g, kw, stages);
+    const int64_t tiles = GROUPED ? 1 : ceil_div(g.R, 16 * FA);  // of rows; workgroups of each
+    const int64_t blocks = std::min(ceil_div(items, kMxNarrowWaves / kw), std::max<int64_t>(1, compute_units() / tiles));
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks, (unsigned)tiles), dim3(64 * kMxNarrowWaves), C::lds(g.E), stream, g, kw, stages);
     return launched();
 }
 
-// The narrow kernel's sizes: rows of a product, units of a wave's registers of
-// A, 32-bit offsets.
-constexpr int kNarrowRows = 32, kNarrowStages = 4;
+// The narrow kernel's sizes: rows of a product (more only where the tiles are
+// few), stages of a wave's registers of A, 32-bit offsets.
+constexpr int kNarrowRows = 32, kNarrowMaxRows = 4096, kNarrowStages = 4;
 
 bool narrow_serves(const MxArgs &g)
 {
     if (g.offsets != nullptr)
         return g.R <= kMxNarrowRows && g.E <= kMxNarrowGroups && (int64_t)g.T * g.U * kMxUnitCodes <= INT32_MAX &&
                ceil_div(g.N, 16) * (g.R + g.E) <= INT32_MAX / 16;
-    return g.R <= kNarrowRows && g.U <= 4 * kMxNarrowWaves * kNarrowStages && g.N <= INT32_MAX / 32;
+    return g.R <= kNarrowMaxRows && g.U <= 4 * kMxNarrowWaves * kNarrowStages && g.N <= INT32_MAX / 32;
+}
+
+// How the narrow kernel would run: waves to a strip, stages of each, time in us.
+struct NarrowPlan {
+    int kw, stages;
+    double time;
+};
+// A strip costs its stages and 1.2 more for its sums and what leads to it, so
+// fewer waves for many strips, more where a wave has one.  MI355X, 24 groups of
+// 4096 x 4096: 59.8 us with 8 waves, 45.7 with 4, 37.0 with 2; 16 x 28672 x
+// 8192: 26.4 us with 8, 24.0 with 4.
+NarrowPlan plan_narrow(const MxArgs &g, int64_t cu)
+{
+    const bool grouped = g.offsets != nullptr;
+    const int64_t strips = ceil_div(g.N, 16) * (grouped ? std::min(g.E, g.R) : 1);
+    const int64_t per_tile = grouped ? cu : std::max<int64_t>(1, cu / ceil_div(g.R, g.R <= 16 ? 16 : 32));  // workgroups
+    NarrowPlan best{kMxNarrowWaves, 1, 0};
+    for (int w = kMxNarrowWaves; w > 0; w /= 2) {
+        int64_t s = std::max<int64_t>(1, ceil_div(g.U, 4 * w));
+        if (!grouped && s > kNarrowStages) continue;
+        if (!grouped && s == 3) s = 4;  // registers for 1, 2 or 4
+        const double t = 1.35 * (double)ceil_div(strips, per_tile * (kMxNarrowWaves / w)) * ((double)s + 1.2);
+        if (best.time == 0 || t < best.time) best = {w, (int)s, t};
+    }
+    return best;
 }
 
 template <int OUT>
 lpgemm_status launch_narrow_any(const MxArgs &g, hipStream_t stream)
 {
-    // Waves to a strip: a strip costs its stages and 1.2 more for its sums and
-    // what leads to it, so fewer waves for many strips, more where a wave has
-    // one.  MI355X, 24 groups of 4096 x 4096: 59.8 us with 8 waves, 45.7 with 4,
-    // 37.0 with 2; 16 x 28672 x 8192: 26.4 us with 8, 24.0 with 4.
-    const int64_t strips = ceil_div(g.N, 16) * (g.offsets ? std::min(g.E, g.R) : 1);
-    int kw = 8, stages = 1;
-    int64_t least = INT64_MAX;
-    for (int w = kMxNarrowWaves; w > 0; w /= 2) {
-        const int64_t s = std::max<int64_t>(1, ceil_div(g.U, 4 * w));
-        const int64_t cost = ceil_div(strips, (int64_t)compute_units() * (kMxNarrowWaves / w)) * (5 * s + 6);
-        if ((g.offsets == nullptr && s > kNarrowStages) || cost >= least) continue;
-        least = cost;
-        kw = w;
-        stages = (int)s;
-    }
+    const NarrowPlan p = plan_narrow(g, compute_units());
+    const int kw = p.kw, stages = p.stages;
     if (g.offsets != nullptr) return launch_narrow<1, 1, true, OUT>(g, kw, stages, stream);
     if (g.R <= 16)
         return stages == 1   ? launch_narrow<1, 1, false, OUT>(g, kw, 1, stream)
@@ -195,10 +208,12 @@ constexpr Shape kShapes[] = {{64, 64, 4, {0.25}, 1.2},
                              {128, 128, 2, {0.42, 0.58}, 1.5},
                              {128, 128, 4, {0.50, 0.62}, 2.0},
                              {256, 256, 2, {0.80, 1.10, 1.45, 1.75}, 11.0}};
+// A ring of two stages hides a copy's way only behind a second workgroup.
+constexpr double kAlone = 1.6;
 enum { kShape64, kShape64x128, kShape128, kShape128Deep, kShape256, kShapeCount };
 
-// The shape that should take the least time for R rows in `groups` equal groups.
-int choose_shape(const MxArgs &g, int64_t cu)
+// The shape that should take the least time for R rows in equal groups; *time in us.
+int choose_shape(const MxArgs &g, int64_t cu, double *time)
 {
     const int64_t groups = g.offsets ? std::min(g.E, g.R) : 1, rows = ceil_div(g.R, groups), stages = ceil_div(g.U, 2);
     int best = kShape64;
@@ -209,12 +224,14 @@ int choose_shape(const MxArgs &g, int64_t cu)
         const int64_t c = ceil_div(rows, s.high), blocks = ceil_div(ceil_div(rows, 64), c);  // tiles of a group, their height / 64
         const int64_t tiles = groups * c * ceil_div(g.N, s.wide);
         if (i == kShape128Deep && tiles > cu) continue;  // one to a compute unit
-        const double t = (double)ceil_div(tiles, cu) * ((double)stages * s.stage[blocks - 1] + s.tile);
+        const double per_stage = s.stage[blocks - 1] * (i != kShape256 && s.stages == 2 && tiles <= cu ? kAlone : 1.0);
+        const double t = (double)ceil_div(tiles, cu) * ((double)stages * per_stage + s.tile);
         if (i == 0 || t < least) {
             best = i;
             least = t;
         }
     }
+    *time = least;
     return best;
 }
 
@@ -233,16 +250,30 @@ lpgemm_status launch_shape(const MxArgs &g, int shape, hipStream_t stream)
     }
 }
 
+// Whether the narrow kernel takes a call that it can serve.  Few rows are its
+// own (grouped: up to eight a group on average); beyond, it wins where the tiles
+// are few and K long, as its waves split K (us, 64 x 64 tiles / narrow):
+//     96 x 80 x 5753        10.4 /  6.0        200 x 300 x 8192     12.8 /  8.9
+//     100 x 100 x 16384     22.9 / 13.1        1000 x 64 x 16384    22.2 / 14.2
+//     64 x 8192 x 8192      13.3 / 18.1        333 x 1001 x 2897     7.5 /  8.5
+bool narrow_pays(const MxArgs &g, int64_t cu, double tiled)
+{
+    if (g.offsets != nullptr) return g.R <= 8 * (int64_t)g.E;
+    return g.R <= kNarrowRows || plan_narrow(g, cu).time + 0.5 < tiled;
+}
+
 template <int OUT>
 lpgemm_status launch_product(const MxArgs &g, hipStream_t stream)
 {
     const int64_t cu = compute_units();
-    switch (forced_kernel()) {
-    case LPGEMM_KERNEL_AUTO:
-        // grouped: up to eight rows a group on average
-        if (narrow_serves(g) && (g.offsets == nullptr || g.R <= 8 * (int64_t)g.E)) return launch_narrow_any<OUT>(g, stream);
-        return launch_shape<OUT>(g, choose_shape(g, cu), stream);
-    case LPGEMM_KERNEL_TILED: return launch_shape<OUT>(g, choose_shape(g, cu), stream);
+    const int forced = forced_kernel();
+    if (forced == LPGEMM_KERNEL_AUTO || forced == LPGEMM_KERNEL_TILED) {
+        double time = 0;
+        const int shape = choose_shape(g, cu, &time);
+        if (forced == LPGEMM_KERNEL_AUTO && narrow_serves(g) && narrow_pays(g, cu, time)) return launch_narrow_any<OUT>(g, stream);
+        return launch_shape<OUT>(g, shape, stream);
+    }
+    switch (forced) {
     case LPGEMM_KERNEL_TILED_64: return launch_shape<OUT>(g, kShape64, stream);
     case LPGEMM_KERNEL_TILED_128: return launch_shape<OUT>(g, g.R * (int64_t)g.N > 128 * 128 * cu ? kShape128 : kShape128Deep, stream);
     case LPGEMM_KERNEL_TILED_256: return launch_shape<OUT>(g, kShape256, stream);

@@ -83,7 +83,7 @@ def test_tiled_many_groups(torch, forced, tile):  # noqa: F811
 # ---- the narrow kernel ----------------------------------------------------------
 # K around each number of waves that split it (4, 8, 16 units) and of stages a wave holds; strips that end past N
 NARROW = [(1, 1, 1), (2, 15, 100), (16, 16, 512), (17, 17, 513), (32, 33, 640), (5, 100, 1024), (9, 250, 1025), (31, 48, 2048), (16, 4000, 2049),
-          (3, 300, 4096), (32, 5000, 4097), (16, 100, 8192), (20, 31, 8193), (1, 9000, 300), (32, 500, 16384), (7, 4, 16300), (12, 70000, 384)]
+          (3, 300, 4096), (33, 40, 700), (65, 130, 4000), (100, 100, 16384), (1000, 64, 2000), (32, 5000, 4097), (16, 100, 8192), (20, 31, 8193), (1, 9000, 300), (32, 500, 16384), (7, 4, 16300), (12, 70000, 384)]
 
 
 @pytest.mark.parametrize("kind", ["float32", "bfloat16", "float16"])
@@ -129,6 +129,6 @@ def test_narrow_many_groups(torch, forced):  # noqa: F811
 def test_narrow_refuses_what_it_does_not_serve(torch, forced):  # noqa: F811
     forced(L.KERNEL_SKINNY)
     z = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda")  # noqa: E731
-    for M, U in ((33, 4), (4, 129)):
+    for M, U in ((4097, 4), (4, 129)):
         with pytest.raises(L.LpgemmError):
             L.lpgemm_mxfp4(z(M, 64 * U), z(M, 4 * U), z(8, 64 * U), z(8, 4 * U))
