@@ -442,8 +442,8 @@ lpgemm_status lpgemm_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scale
  * binary32's normal range.  A block of scale 255 makes its row (A) or column
  * (B) of D NaN.  K == 0 writes zeros.
  * lpgemm_mxfp4_workspace_size gives the bytes of scratch memory that a call
- * can use to split K over more workgroups; the workspace is 256-byte aligned,
- * and with less than that, or none (null, 0), the call runs without.
+ * can use; no kernel uses any at present, so it is 0.  A workspace that is
+ * passed is 256-byte aligned, and a call runs without one (null, 0).
  * LPGEMM_ERR_INVALID_ARG for negative sizes, another out_dtype, a null or
  * misaligned pointer that would be dereferenced; LPGEMM_ERR_UNSUPPORTED above
  * the limits; LPGEMM_ERR_HIP if a launch failed.
@@ -491,6 +491,10 @@ typedef enum lpgemm_kernel LPGEMM_ENUM_BASE {
     LPGEMM_KERNEL_FP6 = 7        /* int4 x int4: A, B re-encoded as FP6 E3M2,    */
                                  /* 256 x 256 tiles on the FP6 matrix cores       */
 } lpgemm_kernel;
+/* The mxfp4 products have TILED, TILED_64, TILED_128, TILED_256 (tiles of up to
+ * that many rows and columns) and SKINNY (product: K <= 16384, up to 4096 rows;
+ * grouped: up to 896 rows of D and 512 groups); anything else forced on them is
+ * LPGEMM_ERR_UNSUPPORTED. */
 /* LPGEMM_KERNEL_AUTO picks FP6 for int4 x int4 when the fast path applies,
  * the call's workspace holds the re-encoded operands, M > 128, and either the
  * 256 x 256 output tiles number at least twice the compute units with

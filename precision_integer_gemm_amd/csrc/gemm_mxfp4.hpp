@@ -2,7 +2,20 @@
 //     D[m][n] = out( sum_j 2^(sa[m][j] - 127) 2^(sb[n][j] - 127) sum_{k in block j} a[m][k] b[n][k] )
 // over blocks of 32 k, one pair of matrices or one matrix of B per group of
 // rows.  gfx950's v_mfma_scale_f32_*_f8f6f4 multiplies e2m1 operands with one
-// e8m0 scale byte per row and block: the format's definition, in one instruction.
+// e8m0 scale byte per row and block: the format's definition, in one
+// instruction.  Products of a block are exact and sums are binary32; the one
+// rounding to fewer bits is that of the result.
+//
+// Three kernels (the choice between them: mxfp4_api.hip):
+//  - tiled, 64 x 64 to 128 x 128 tiles: bound by what a compute unit draws from
+//    its L2 and beyond (60-100 GB/s): 1110 rows on 13 groups of 1001 x 2897
+//    12.8 us, 4096 on 64 of 2048 x 4096 77 us (3.9 TB/s), 333 x 1001 x 2897 7.4 us.
+//  - large, tiles of 256 columns: bound by the matrix cores at the clock they
+//    run at (1.7 GHz, 58% busy on 8192^3): 268 us, 4.1 PFLOP/s; 3000 x 5120 x
+//    6144 51 us, 16384 rows on 32 groups of 4096 x 4096 200 us (2.7 PFLOP/s).
+//  - narrow, few rows: bound by memory: 16 x 28672 x 8192 23.9 us (5.3 TB/s), 64
+//    rows on 24 of 32 groups of 4096 x 4096 37 us (5.8 TB/s), 1 x 4096 x 4096
+//    4.3 us on the device.
 #pragma once
 
 #include "device_common.hpp"

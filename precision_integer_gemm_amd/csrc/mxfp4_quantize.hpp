@@ -8,6 +8,11 @@
 // to the even code, and magnitudes above 6 become 6; bit 3 is the sign.  With
 // E the exponent field of a in binary32, the scale byte is max(E, 2) - 2.  A
 // block that holds a NaN or an infinity gets scale byte 255 (NaN) and codes 0.
+//
+// Bound by memory: 8192 x 8192 fp32 65 us (4.7 TB/s read and written), back to
+// bf16 26 us (6.6 TB/s; its codes come from the caches).  With seven compares a
+// value in place of the conversion instructions and a 64-bit division for
+// each item both took 197 us.  A row of 8192 takes 2 us; the call, 5 us.
 #pragma once
 
 #include "device_common.hpp"
