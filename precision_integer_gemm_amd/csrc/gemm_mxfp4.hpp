@@ -355,28 +355,37 @@ struct MxTile {
     // scales of two stages: 1 KB a wave, of its 32 FN rows; two pairs are in flight, and the one being read
     static constexpr int kPairs = kStages / 2 + 1, kScales = 4096;
     static constexpr int kRing = kStages * kCodes + kPairs * kScales;
-    static constexpr int lds(int groups) { return kRing + 4 * (groups + 1 + 4); }
+    static constexpr int lds(int groups, int kgroups) { return kgroups * kRing + 4 * (groups + 1 + 4 * kgroups); }
 };
 
-template <int HM, int FN, int STAGES, int OUT>
-__global__ __launch_bounds__(256, 2) void gemm_mxfp4_tiled_kernel(MxArgs g, int tiles_n, int xcds)
+// KG == 2: eight waves, the second four on the second half of K with a ring of
+// their own; their sums are added at the end, through LDS.  A stage of a small
+// tile is a chain of waits (a copy's, a barrier's, a fragment's: 0.25 us, of
+// which its MFMAs are 0.06), so where there is one tile to a compute unit two
+// chains side by side are shorter, by what the copies leave: 60 x 60 x 16384
+// 22.0 -> 16.6 us, 1024 x 1024 x 4096 9.6 -> 8.9 us.
+template <int HM, int FN, int STAGES, int KG, int OUT>
+__global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void gemm_mxfp4_tiled_kernel(MxArgs g, int tiles_n, int xcds)
 {
     using T = MxTile<HM, FN, STAGES>;
     static_assert(4 * mx_stage_bytes<OUT, FN>() <= T::kStages * T::kCodes, "the ring holds the rows on their way out");
     constexpr int ST = T::kStages;
-    extern __shared__ __align__(1024) uint8_t smem[];
-    int32_t *cum = reinterpret_cast<int32_t *>(smem + T::kRing);  // [E + 1]: row tiles before group e
+    extern __shared__ __align__(1024) uint8_t smem_all[];
+    int32_t *cum = reinterpret_cast<int32_t *>(smem_all + KG * T::kRing);  // [E + 1]: row tiles before group e
 
     const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3;
+    const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid >> 8);
+    uint8_t *smem = smem_all + kg * T::kRing;
     const int wm = wave >> 1, wn = wave & 1;
     const int r32 = lane & 31, h = lane >> 5;
-    const int U = g.U, ktiles = (U + 1) / 2;
+    // this half's stages: k0 .. k0 + ktiles - 1, whole pairs (scales come for two)
+    const int U = g.U, ktiles = KG == 1 ? (U + 1) / 2 : 2 * ((U + 7) / 8), k0 = kg * ktiles;
     const uint32_t ldc = (uint32_t)U * kMxUnitCodes, lds_ = (uint32_t)U * kMxUnitScales;
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(smem);
 
     MxGroups groups;
-    if (g.offsets != nullptr) groups.init<4>(g, 64 * HM, cum);
+    if (g.offsets != nullptr) groups.init<4 * KG>(g, 64 * HM, cum);
     const int total = (g.offsets == nullptr ? (g.R + 64 * HM - 1) / (64 * HM) : groups.total) * tiles_n;
 
     // The current tile: group e, rows [m0, m1) of D, columns from n0, height 64 fm.
@@ -421,7 +430,8 @@ __global__ __launch_bounds__(256, 2) void gemm_mxfp4_tiled_kernel(MxArgs g, int 
 
     // Copy j of stage kt's copies into its slot, for tiles of height 64 f.
     // Units past the row read zeros.
-    auto issue = [&](int j, int f, int kt, uint32_t base) __attribute__((always_inline)) {
+    auto issue = [&](int j, int f, int local, uint32_t base) __attribute__((always_inline)) {
+        const int kt = k0 + local;
         const uint32_t koff = (uint32_t)kt * 128u;
         if (j < T::NB) {
             const int p = wave * T::NB + j;
@@ -437,8 +447,9 @@ __global__ __launch_bounds__(256, 2) void gemm_mxfp4_tiled_kernel(MxArgs g, int 
     // no window of 16 bytes: theirs are written by hand, and these copies bring
     // zeros to a place that is not read.
     auto issue_scales = [&](int q) __attribute__((always_inline)) {
-        const bool copied = U >= 4 && 4 * q < U;
-        mx_dma16_at(rsrc_s, copied ? s_off : kOutOfRange, (uint32_t)mx_scale_window(q, U) * 4u,
+        const int at = k0 / 2 + q;
+        const bool copied = U >= 4 && 4 * at < U;
+        mx_dma16_at(rsrc_s, copied ? s_off : kOutOfRange, (uint32_t)mx_scale_window(at, U) * 4u,
                     lds0 + (uint32_t)(ST * T::kCodes + (U >= 4 ? q % T::kPairs : 1) * T::kScales) + (uint32_t)wave * 1024u);
     };
     // dispatch on the height; bodies see it as a constant
@@ -497,7 +508,7 @@ __global__ __launch_bounds__(256, 2) void gemm_mxfp4_tiled_kernel(MxArgs g, int 
         // row r of a half of FN blocks sits in that half's wave's kilobyte;
         // A's rows are dealt out by FN blocks whatever the tile's height
         auto read_scales = [&](int kt) __attribute__((always_inline)) {
-            const int q = kt >> 1, d = mx_scale_at(2 * kt + h, q, U);
+            const int q = kt >> 1, d = mx_scale_at(2 * (k0 + kt) + h, k0 / 2 + q, U);
             const uint8_t *base = smem + ST * T::kCodes + (q % T::kPairs) * T::kScales + 4 * d;
 #pragma unroll
             for (int i = 0; i < FN; ++i)
@@ -571,10 +582,30 @@ __global__ __launch_bounds__(256, 2) void gemm_mxfp4_tiled_kernel(MxArgs g, int 
         prologue();
         with_height(contract);
         lds_barrier();  // every wave is done with the ring
+        if (KG == 2) {
+            // the second half's sums, 16 bytes a lane at a time
+            i32x4 *sums = reinterpret_cast<i32x4 *>(smem_all + T::kRing) + wave * (HM * FN * 4 * 64) + lane;
+#pragma unroll
+            for (int i = 0; i < HM * FN * 4; ++i) {
+                const f32x16 &x = acc[i / 4 % FN][i / 4 / FN];
+                if (kg == 1)
+                    sums[i * 64] = i32x4{__float_as_int(x[4 * (i % 4)]), __float_as_int(x[4 * (i % 4) + 1]),
+                                         __float_as_int(x[4 * (i % 4) + 2]), __float_as_int(x[4 * (i % 4) + 3])};
+            }
+            lds_barrier();
+            if (kg == 0) {
+#pragma unroll
+                for (int i = 0; i < HM * FN * 4; ++i) {
+                    const i32x4 y = sums[i * 64];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[i / 4 % FN][i / 4 / FN][4 * (i % 4) + q] += __int_as_float(y[q]);
+                }
+            }
+        }
         uint8_t *out_stage = smem + wave * mx_stage_bytes<OUT, FN>();
 #pragma unroll
         for (int f = 0; f < HM; ++f) {
-            if (f >= fm) break;
+            if (f >= fm || kg != 0) break;
             mx_store_rows<OUT, FN>(g, out_stage, [&](int w) -> const f32x16 & { return acc[w][f]; }, m0 + (wm * fm + f) * 32, m1,
                                    n0 + wn * FN * 32);
         }

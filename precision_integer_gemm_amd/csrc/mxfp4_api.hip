@@ -88,20 +88,20 @@ lpgemm_status allow_lds(Kernel kernel, int bytes, std::once_flag *once, hipError
     return err[dev] == hipSuccess ? LPGEMM_OK : LPGEMM_ERR_HIP;
 }
 
-template <int HM, int FN, int STAGES, int OUT>
+template <int HM, int FN, int STAGES, int KG, int OUT>
 lpgemm_status launch_tiled(const MxArgs &g, hipStream_t stream)
 {
     using T = MxTile<HM, FN, STAGES>;
     static std::once_flag once[kMaxDevices];
     static hipError_t err[kMaxDevices];
-    const auto kernel = &gemm_mxfp4_tiled_kernel<HM, FN, STAGES, OUT>;
-    const lpgemm_status st = allow_lds(kernel, T::lds(LPGEMM_MXFP4_MAX_GROUPS), once, err);
+    const auto kernel = &gemm_mxfp4_tiled_kernel<HM, FN, STAGES, KG, OUT>;
+    const lpgemm_status st = allow_lds(kernel, T::lds(LPGEMM_MXFP4_MAX_GROUPS, KG), once, err);
     if (st != LPGEMM_OK) return st;
     const int tiles_n = (int)ceil_div(g.N, 64 * FN);
     // at most one ragged row tile a group more than the rows fill
     const int64_t most = (ceil_div(g.R, 64 * HM) + (g.offsets ? std::min(g.E, g.R) : 0)) * tiles_n;
-    const unsigned blocks = (unsigned)std::min<int64_t>(most, (T::lds(g.E) > 80 * 1024 ? 1 : 2) * (int64_t)compute_units());
-    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), T::lds(g.E), stream, g, tiles_n, kXcds);
+    const unsigned blocks = (unsigned)std::min<int64_t>(most, (T::lds(g.E, KG) > 80 * 1024 ? 1 : 2) * (int64_t)compute_units());
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256 * KG), T::lds(g.E, KG), stream, g, tiles_n, kXcds);
     return launched();
 }
 
@@ -199,18 +199,22 @@ lpgemm_status launch_narrow_any(const MxArgs &g, hipStream_t stream)
 //     199 x 8582 x 6277       23 /   22 /   23 /   19 /  40
 //     2848 x 2880 x 3200      41 /   39 /   34 /   36 /  31
 //     4096 x 4096 x 4096      88 /    - /   50 /    - /  41
+// 64 x 64 with K in one / two halves: 1024 x 1024 x 4096 9.6 / 8.9, 2000 x 200
+// x 4096 8.9 / 7.9, 333 x 1001 x 2897 7.5 / 7.5, 700 x 1400 x 2560 7.6 / 7.9.
 struct Shape {
     int high, wide, stages;
     double stage[4], tile;
 };
 constexpr Shape kShapes[] = {{64, 64, 4, {0.25}, 1.2},
+                             {64, 64, 4, {0.21}, 1.7},  // K in two halves side by side
                              {64, 128, 2, {0.42}, 1.1},
                              {128, 128, 2, {0.42, 0.58}, 1.5},
                              {128, 128, 4, {0.50, 0.62}, 2.0},
                              {256, 256, 2, {0.80, 1.10, 1.45, 1.75}, 11.0}};
+constexpr int kSplitUnits = 8;  // two pairs of stages for each half
 // A ring of two stages hides a copy's way only behind a second workgroup.
 constexpr double kAlone = 1.6;
-enum { kShape64, kShape64x128, kShape128, kShape128Deep, kShape256, kShapeCount };
+enum { kShape64, kShape64Split, kShape64x128, kShape128, kShape128Deep, kShape256, kShapeCount };
 
 // The shape that should take the least time for R rows in equal groups; *time in us.
 int choose_shape(const MxArgs &g, int64_t cu, double *time)
@@ -223,7 +227,8 @@ int choose_shape(const MxArgs &g, int64_t cu, double *time)
         if (i == kShape256 && g.U < MxLarge::kMinUnits) continue;
         const int64_t c = ceil_div(rows, s.high), blocks = ceil_div(ceil_div(rows, 64), c);  // tiles of a group, their height / 64
         const int64_t tiles = groups * c * ceil_div(g.N, s.wide);
-        if (i == kShape128Deep && tiles > cu) continue;  // one to a compute unit
+        if ((i == kShape128Deep || i == kShape64Split) && tiles > cu) continue;  // one to a compute unit
+        if (i == kShape64Split && g.U < kSplitUnits) continue;
         const double per_stage = s.stage[blocks - 1] * (i != kShape256 && s.stages == 2 && tiles <= cu ? kAlone : 1.0);
         const double t = (double)ceil_div(tiles, cu) * ((double)stages * per_stage + s.tile);
         if (i == 0 || t < least) {
@@ -242,11 +247,12 @@ lpgemm_status launch_shape(const MxArgs &g, int shape, hipStream_t stream)
     const Shape &s = kShapes[shape];
     if (ceil_div(g.R, s.high) + g.E > INT32_MAX / ceil_div(g.N, s.wide)) return LPGEMM_ERR_UNSUPPORTED;
     switch (shape) {
-    case kShape64: return launch_tiled<1, 1, 4, OUT>(g, stream);
-    case kShape64x128: return launch_tiled<1, 2, 2, OUT>(g, stream);
-    case kShape128: return launch_tiled<2, 2, 2, OUT>(g, stream);
-    case kShape128Deep: return launch_tiled<2, 2, 4, OUT>(g, stream);
-    default: return g.U >= MxLarge::kMinUnits ? launch_large<OUT>(g, stream) : launch_tiled<2, 2, 2, OUT>(g, stream);
+    case kShape64: return launch_tiled<1, 1, 4, 1, OUT>(g, stream);
+    case kShape64Split: return launch_tiled<1, 1, 4, 2, OUT>(g, stream);
+    case kShape64x128: return launch_tiled<1, 2, 2, 1, OUT>(g, stream);
+    case kShape128: return launch_tiled<2, 2, 2, 1, OUT>(g, stream);
+    case kShape128Deep: return launch_tiled<2, 2, 4, 1, OUT>(g, stream);
+    default: return g.U >= MxLarge::kMinUnits ? launch_large<OUT>(g, stream) : launch_tiled<2, 2, 2, 1, OUT>(g, stream);
     }
 }
 
@@ -274,7 +280,7 @@ lpgemm_status launch_product(const MxArgs &g, hipStream_t stream)
         return launch_shape<OUT>(g, shape, stream);
     }
     switch (forced) {
-    case LPGEMM_KERNEL_TILED_64: return launch_shape<OUT>(g, kShape64, stream);
+    case LPGEMM_KERNEL_TILED_64: return launch_shape<OUT>(g, g.R * (int64_t)g.N > 64 * 64 * cu || g.U < kSplitUnits ? kShape64 : kShape64Split, stream);
     case LPGEMM_KERNEL_TILED_128: return launch_shape<OUT>(g, g.R * (int64_t)g.N > 128 * 128 * cu ? kShape128 : kShape128Deep, stream);
     case LPGEMM_KERNEL_TILED_256: return launch_shape<OUT>(g, kShape256, stream);
     case LPGEMM_KERNEL_SKINNY: return narrow_serves(g) ? launch_narrow_any<OUT>(g, stream) : LPGEMM_ERR_UNSUPPORTED;
