@@ -247,30 +247,6 @@ __device__ __forceinline__ void mx_store4(void *d, int64_t at, int n, int N, flo
     }
 }
 
-// One 32 x 32 block of D: row m, columns from nb; rows from m1 and columns from
-// N on are skipped.  bf16 and fp16 exchange halves, so that a lane has eight
-// neighbouring columns of its row.
-template <int OUT>
-__device__ __forceinline__ void mx_store_block(const MxArgs &g, const f32x16 &c, int m, int m1, int nb, int h)
-{
-    const int64_t at = (int64_t)m * g.N;
-    if (OUT != OUT_F32) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const uint32_t x0 = mx_pack2<OUT>(c[8 * q + 0], c[8 * q + 1]), x1 = mx_pack2<OUT>(c[8 * q + 2], c[8 * q + 3]);
-            const uint32_t y0 = mx_pack2<OUT>(c[8 * q + 4], c[8 * q + 5]), y1 = mx_pack2<OUT>(c[8 * q + 6], c[8 * q + 7]);
-            const auto s0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
-            const auto s1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
-            if (m < m1)
-                mx_store8<OUT>(g.D, at, nb + 16 * q + 8 * h, g.N, i32x4{(int32_t)s0[0], (int32_t)s1[0], (int32_t)s0[1], (int32_t)s1[1]});
-        }
-    } else if (m < m1) {
-#pragma unroll
-        for (int rg = 0; rg < 4; ++rg)
-            mx_store4<OUT>(g.D, at, nb + 8 * rg + 4 * h, g.N, c[4 * rg], c[4 * rg + 1], c[4 * rg + 2], c[4 * rg + 3]);
-    }
-}
-
 // 32 rows x 32 W columns of D, blocks c(0) .. c(W - 1) side by side, through the
 // wave's own `stage` of LDS (mx_stage_bytes), so that a store instruction writes
 // whole rows of them.  In the MFMA's layout it writes 32 bytes of each of 32
@@ -736,7 +712,6 @@ __global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int 
     find(v);
     place();
     prologue();
-    int pending = 0;  // store instructions of the previous tile, at least
 
     auto run_tile = [&](auto height) __attribute__((always_inline)) {
         constexpr int FM = decltype(height)::value;
@@ -781,12 +756,7 @@ __global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int 
         };
 
         // stage 0 into registers, then its place to stage 2
-        if (pending >= 32)
-            wait_vmcnt<16 + 32>();
-        else if (pending >= 16)
-            wait_vmcnt<16 + 16>();
-        else
-            wait_vmcnt<16>();
+        wait_vmcnt<16>();
         lds_barrier();
 #pragma unroll
         for (int s = 0; s < 4; ++s)
@@ -855,29 +825,19 @@ __global__ __launch_bounds__(256, 1) void gemm_mxfp4_large_kernel(MxArgs g, int 
         const int tm0 = m0, tm1 = m1, tn0 = n0;
         v += (int)gridDim.x;
         lds_barrier();  // every wave is done with the ring
-        if (v < total) {
-            find(v);
-            place();
-            prologue();
-        } else if (OUT != OUT_F32) {
-            // no copies follow: the ring is free for whole rows (fp32 values, in
-            // both branches unchanged, would be taken out of the accumulators
-            // ahead of the branch and spilled)
-            uint8_t *out_stage = smem + wave * mx_stage_bytes<OUT, 4>();
-#pragma unroll
-            for (int f = 0; f < FM; ++f)
-                mx_store_rows<OUT, 4>(g, out_stage, [&](int w) -> const f32x16 & { return acc[w][f]; }, tm0 + (wm * FM + f) * 32, tm1,
-                                      tn0 + wn * 128);
-            return;
-        }
-        const int sl = opaque_lane();
+        // Whole rows through the ring, then the next tile's first copies.  The
+        // other way round, results in the MFMA's layout behind the copies, 16-bit
+        // types took as long and fp32 far longer (8192 x 8192 x 4096: 272 / 190 us).
+        uint8_t *out_stage = smem + wave * mx_stage_bytes<OUT, 4>();
 #pragma unroll
         for (int f = 0; f < FM; ++f)
-#pragma unroll
-            for (int fn = 0; fn < 4; ++fn)
-                mx_store_block<OUT>(g, acc[fn][f], tm0 + (wm * FM + f) * 32 + (sl & 31), tm1, tn0 + (wn * 4 + fn) * 32, sl >> 5);
-        const bool full = tm0 + 64 * FM <= tm1 && tn0 + 256 <= g.N;
-        pending = full ? 4 * FM * (OUT == OUT_F32 ? 4 : 2) : 0;
+            mx_store_rows<OUT, 4>(g, out_stage, [&](int w) -> const f32x16 & { return acc[w][f]; }, tm0 + (wm * FM + f) * 32, tm1,
+                                  tn0 + wn * 128);
+        if (v >= total) return;
+        lds_barrier();  // every wave's rows have left
+        find(v);
+        place();
+        prologue();
     };
 
     while (v < total) {

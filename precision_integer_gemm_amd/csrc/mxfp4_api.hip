@@ -208,12 +208,14 @@ struct Shape {
 constexpr Shape kShapes[] = {{64, 64, 4, {0.25}, 1.2},
                              {64, 64, 4, {0.21}, 1.7},  // K in two halves side by side
                              {64, 128, 2, {0.42}, 1.1},
-                             {128, 128, 2, {0.42, 0.58}, 1.5},
+                             {128, 128, 2, {0.45, 0.70}, 1.5},
                              {128, 128, 4, {0.50, 0.62}, 2.0},
-                             {256, 256, 2, {0.80, 1.10, 1.45, 1.75}, 11.0}};
+                             {256, 256, 2, {0.80, 1.10, 1.45, 1.75}, 9.0}};
 constexpr int kSplitUnits = 8;  // two pairs of stages for each half
 // A ring of two stages hides a copy's way only behind a second workgroup.
 constexpr double kAlone = 1.6;
+// And groups' matrices come from further away than a product's shared columns.
+constexpr double kGrouped = 1.15;
 enum { kShape64, kShape64Split, kShape64x128, kShape128, kShape128Deep, kShape256, kShapeCount };
 
 // The shape that should take the least time for R rows in equal groups; *time in us.
@@ -229,7 +231,8 @@ int choose_shape(const MxArgs &g, int64_t cu, double *time)
         const int64_t tiles = groups * c * ceil_div(g.N, s.wide);
         if ((i == kShape128Deep || i == kShape64Split) && tiles > cu) continue;  // one to a compute unit
         if (i == kShape64Split && g.U < kSplitUnits) continue;
-        const double per_stage = s.stage[blocks - 1] * (i != kShape256 && s.stages == 2 && tiles <= cu ? kAlone : 1.0);
+        const bool two = i != kShape256 && s.stages == 2;
+        const double per_stage = s.stage[blocks - 1] * (two && tiles <= cu ? kAlone : 1.0) * (two && g.offsets ? kGrouped : 1.0);
         const double t = (double)ceil_div(tiles, cu) * ((double)stages * per_stage + s.tile);
         if (i == 0 || t < least) {
             best = i;
