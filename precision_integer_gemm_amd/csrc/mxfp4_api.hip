@@ -46,6 +46,11 @@ lpgemm_status check_values(const void *x, const void *codes, const void *scales,
 // Items of eight values; four a thread where that leaves four workgroups a
 // compute unit, else one.
 constexpr int64_t kManyItems = 4 * 256 * 4 * 256;
+// Values of more bytes than this do not stay in the 256 MB last-level cache
+// between a call and the next: they pass by it.  To codes and back, MI355X:
+// 16384 x 8192 bf16 (268 MB) 140 us kept, 108 passed by; 3001 x 8191 fp16 (49
+// MB, from the cache) 24.7 kept, 28.6 passed by.
+constexpr int64_t kPastCaches = 192 << 20;
 
 template <int IN>
 lpgemm_status launch_quantize(const void *x, int64_t ldx, uint8_t *codes, uint8_t *scales, int64_t rows, int64_t K, hipStream_t stream)
@@ -54,7 +59,8 @@ lpgemm_status launch_quantize(const void *x, int64_t ldx, uint8_t *codes, uint8_
     const bool many = total >= kManyItems;
     const int64_t blocks = ceil_div(total, many ? 1024 : 256);
     if (blocks > INT32_MAX) return LPGEMM_ERR_UNSUPPORTED;
-    const auto kernel = many ? &mxfp4_quantize_kernel<IN, 4> : &mxfp4_quantize_kernel<IN, 1>;
+    const bool past = rows * K * (int64_t)element_bytes(IN) > kPastCaches;
+    const auto kernel = past ? &mxfp4_quantize_kernel<IN, 4, true> : many ? &mxfp4_quantize_kernel<IN, 4, false> : &mxfp4_quantize_kernel<IN, 1, false>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, stream, x, ldx, reinterpret_cast<uint32_t *>(codes), scales, rows,
                        (int32_t)K, (uint32_t)items);
     return launched();
@@ -67,7 +73,9 @@ lpgemm_status launch_dequantize(const uint8_t *codes, const uint8_t *scales, voi
     const bool many = total >= kManyItems;
     const int64_t blocks = ceil_div(total, many ? 1024 : 256);
     if (blocks > INT32_MAX) return LPGEMM_ERR_UNSUPPORTED;
-    const auto kernel = many ? &mxfp4_dequantize_kernel<OUT, 4> : &mxfp4_dequantize_kernel<OUT, 1>;
+    // half as large results too: they are written, so the cache has to put them out
+    const bool past = 2 * rows * K * (int64_t)element_bytes(OUT) > kPastCaches;
+    const auto kernel = past ? &mxfp4_dequantize_kernel<OUT, 4, true> : many ? &mxfp4_dequantize_kernel<OUT, 4, false> : &mxfp4_dequantize_kernel<OUT, 1, false>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, stream, reinterpret_cast<const uint32_t *>(codes), scales, y, rows,
                        (int32_t)K, (uint32_t)items);
     return launched();

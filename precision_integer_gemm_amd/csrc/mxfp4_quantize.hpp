@@ -9,10 +9,11 @@
 // E the exponent field of a in binary32, the scale byte is max(E, 2) - 2.  A
 // block that holds a NaN or an infinity gets scale byte 255 (NaN) and codes 0.
 //
-// Bound by memory: 8192 x 8192 fp32 65 us (4.7 TB/s read and written), back to
-// bf16 26 us (6.6 TB/s; its codes come from the caches).  With seven compares a
-// value in place of the conversion instructions and a 64-bit division for
-// each item both took 197 us.  A row of 8192 takes 2 us; the call, 5 us.
+// Bound by memory: 8192 x 8192 fp32 57 us (5.4 TB/s read and written), back to
+// bf16 25 us (6.8 TB/s; its codes come from the caches), 82 us together; 90 with
+// loads and stores that the caches keep, 197 with seven compares a value in
+// place of the conversion instructions and a 64-bit division for each item.
+// A row of 8192 takes 2 us; the call, 5 us.
 #pragma once
 
 #include "device_common.hpp"
@@ -34,26 +35,35 @@ typedef float mx_f32x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ float mx_scale(uint32_t s) { return __uint_as_float(s == 0u ? 0x00400000u : s << 23); }
 
 // 16 bytes at any address of the element's alignment (global memory takes
-// unaligned vector accesses).
+// unaligned vector accesses).  NT: data that no cache will keep anyway passes
+// by them, so that the codes stay.
+typedef u32x4 mx_loose __attribute__((aligned(2)));
+template <bool NT>
 __device__ __forceinline__ u32x4 mx_load16(const void *p)
 {
-    u32x4 v;
-    __builtin_memcpy(&v, p, 16);
-    return v;
+    if (NT) return __builtin_nontemporal_load(static_cast<const mx_loose *>(p));
+    return *static_cast<const mx_loose *>(p);
 }
-__device__ __forceinline__ void mx_store16(void *p, u32x4 v) { __builtin_memcpy(p, &v, 16); }
+template <bool NT>
+__device__ __forceinline__ void mx_store16(void *p, u32x4 v)
+{
+    if (NT)
+        __builtin_nontemporal_store(v, static_cast<mx_loose *>(p));
+    else
+        *static_cast<mx_loose *>(p) = v;
+}
 
 // Eight values of a row from k0 on, zeros from K on: IN is OUT_F32, OUT_BF16
 // or OUT_F16; 16-bit types in w[0].
-template <int IN>
+template <int IN, bool NT>
 __device__ __forceinline__ void mx_load8(const void *x, int64_t at, int left, u32x4 (&w)[2])
 {
     w[0] = w[1] = u32x4{0, 0, 0, 0};
     if (IN == OUT_F32) {
         const float *p = static_cast<const float *>(x) + at;
         if (left >= 8) {
-            w[0] = mx_load16(p);
-            w[1] = mx_load16(p + 4);
+            w[0] = mx_load16<NT>(p);
+            w[1] = mx_load16<NT>(p + 4);
         } else {
 #pragma unroll
             for (int j = 0; j < 7; ++j)
@@ -62,7 +72,7 @@ __device__ __forceinline__ void mx_load8(const void *x, int64_t at, int left, u3
     } else {
         const uint16_t *p = static_cast<const uint16_t *>(x) + at;
         if (left >= 8) {
-            w[0] = mx_load16(p);
+            w[0] = mx_load16<NT>(p);
         } else {
 #pragma unroll
             for (int j = 0; j < 7; ++j)
@@ -137,7 +147,7 @@ __device__ __forceinline__ MxItem mx_item(int64_t row0, uint32_t rest, uint32_t 
     return MxItem{row0 + rows, (int32_t)(8 * (rest - rows * items))};
 }
 
-template <int IN, int J>
+template <int IN, int J, bool NT>
 __global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const void *__restrict__ X, int64_t ldx,
                                                              uint32_t *__restrict__ codes,
                                                              uint8_t *__restrict__ scales, int64_t rows,
@@ -154,7 +164,7 @@ __global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const void *__restr
         const uint32_t local = 256 * j + threadIdx.x;
         const MxItem it = mx_item(row0, rest0 + local, items);
         pad[j] = (it.k0 & ~31) >= K;
-        mx_load8<IN>(X, it.row * ldx + it.k0, first + local < total ? K - it.k0 : 0, w[j]);
+        mx_load8<IN, NT>(X, it.row * ldx + it.k0, first + local < total ? K - it.k0 : 0, w[j]);
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -201,7 +211,7 @@ __device__ __forceinline__ void mx_values(uint32_t c, uint32_t s, u32x4 (&w)[2])
     }
 }
 
-template <int OUT, int J>
+template <int OUT, int J, bool NT>
 __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const uint32_t *__restrict__ codes,
                                                                const uint8_t *__restrict__ scales,
                                                                void *__restrict__ Y, int64_t rows, int32_t K,
@@ -229,8 +239,8 @@ __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const uint32_t *_
         if (OUT == OUT_F32) {
             float *p = static_cast<float *>(Y) + at;
             if (left >= 8) {
-                mx_store16(p, w[0]);
-                mx_store16(p + 4, w[1]);
+                mx_store16<NT>(p, w[0]);
+                mx_store16<NT>(p + 4, w[1]);
             } else {
 #pragma unroll
                 for (int k = 0; k < 7; ++k)
@@ -239,7 +249,7 @@ __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const uint32_t *_
         } else {
             uint16_t *p = static_cast<uint16_t *>(Y) + at;
             if (left >= 8) {
-                mx_store16(p, w[0]);
+                mx_store16<NT>(p, w[0]);
             } else {
 #pragma unroll
                 for (int k = 0; k < 7; ++k)
