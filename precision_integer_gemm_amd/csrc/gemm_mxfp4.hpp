@@ -11,10 +11,10 @@
 //    its L2 and beyond (60-100 GB/s): 1110 rows on 13 groups of 1001 x 2897
 //    12.8 us, 4096 on 64 of 2048 x 4096 77 us (3.9 TB/s), 333 x 1001 x 2897 7.4 us.
 //  - large, tiles of 256 columns: bound by the matrix cores at the clock they
-//    run at (1.7 GHz, 58% busy on 8192^3): 268 us, 4.1 PFLOP/s; 3000 x 5120 x
-//    6144 51 us, 16384 rows on 32 groups of 4096 x 4096 200 us (2.7 PFLOP/s).
+//    run at (1.75 GHz, 57% busy on 8192^3): 261 us, 4.2 PFLOP/s; 3000 x 5120 x
+//    6144 51 us, 16384 rows on 32 groups of 4096 x 4096 191 us (2.9 PFLOP/s).
 //  - narrow, few rows: bound by memory: 16 x 28672 x 8192 23.9 us (5.3 TB/s), 64
-//    rows on 24 of 32 groups of 4096 x 4096 37 us (5.8 TB/s), 1 x 4096 x 4096
+//    rows on 24 of 32 groups of 4096 x 4096 36 us (6.0 TB/s), 1 x 4096 x 4096
 //    4.3 us on the device.
 #pragma once
 
