@@ -273,6 +273,10 @@ lpgemm_status launch_shape(const MxArgs &g, int shape, hipStream_t stream)
 //     96 x 80 x 5753        10.4 /  6.0        200 x 300 x 8192     12.8 /  8.9
 //     100 x 100 x 16384     22.9 / 13.1        1000 x 64 x 16384    22.2 / 14.2
 //     64 x 8192 x 8192      13.3 / 18.1        333 x 1001 x 2897     7.5 /  8.5
+// Few rows, best tiles / narrow, weights from memory, as in use: 16 x 28672 x
+// 8192 29.5 / 23.9, 32 x 28672 x 8192 30.3 / 29.4, 16 x 12313 x 7906 15.4 / 14.4,
+// 25 x 12313 x 7906 15.9 / 17.5, 32 x 4096 x 4096 9.1 / 6.2 (weights that the
+// last-level cache holds: 16 x 28672 x 8192 21.2 / 23.0).
 bool narrow_pays(const MxArgs &g, int64_t cu, double tiled)
 {
     if (g.offsets != nullptr) return g.R <= 8 * (int64_t)g.E;
