@@ -464,9 +464,9 @@ lpgemm_status lpgemm_mxfp4_workspace_size(int64_t M, int64_t N, int64_t K, int32
  *   B, SFB    device, codes and scales of E matrices of N rows, one after another
  *   offsets   device, int32 [E + 1], non-decreasing from 0 to R; groups may be
  *             empty.  Read on the device, so a call needs no synchronisation.
- *             Each offset is taken into [0, R] and a decreasing pair is an
- *             empty group, so nothing outside D is written; rows of D in no
- *             group are left as they are.
+ *             Each offset is taken into [0, R], and one below an offset before
+ *             it to that one: no row is in two groups and nothing outside D is
+ *             written.  Rows of D in no group are left as they are.
  *   D         device, [R][N], written
  * Accuracy and errors as for lpgemm_mxfp4; E above LPGEMM_MXFP4_MAX_GROUPS
  * is LPGEMM_ERR_UNSUPPORTED.

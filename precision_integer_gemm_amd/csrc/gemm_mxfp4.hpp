@@ -34,15 +34,18 @@ struct MxArgs {
     int32_t T, R, N, U, E;
 };
 
-// Group e's rows [begin, end), each offset taken into [0, R].
-__device__ __forceinline__ void mx_group(const MxArgs &g, int e, int &begin, int &end)
+// Group e's rows [begin, end): each offset taken into [0, R], and one below an
+// offset before it to that one, so that no row is in two groups and the groups
+// have at most R / height + E row tiles whatever the offsets hold.  `ordered`:
+// no offset is below the one before it; false comes back where e's are not.
+__device__ __forceinline__ bool mx_group(const MxArgs &g, int e, bool ordered, int &begin, int &end)
 {
-    begin = 0;
-    end = g.R;
-    if (g.offsets != nullptr) {
-        begin = min(max(g.offsets[e], 0), g.R);
-        end = min(max(g.offsets[e + 1], begin), g.R);
-    }
+    begin = min(max(g.offsets[e], 0), g.R);
+    if (!ordered)
+        for (int i = 0; i < e; ++i) begin = max(begin, min(g.offsets[i], g.R));
+    const int next = min(max(g.offsets[e + 1], 0), g.R);
+    end = max(begin, next);
+    return next >= begin;
 }
 
 __device__ __forceinline__ i32x8 mx_operand(i32x4 c) { return i32x8{c.x, c.y, c.z, c.w, 0, 0, 0, 0}; }
@@ -86,35 +89,49 @@ __device__ __forceinline__ uint32_t mx_pack2(float a, float b)
 
 // Row tiles of `high` rows before each group, summed into cum[0 .. E], and
 // their number: thread t takes groups t P .. t P + P - 1.  cum has WAVES words
-// more for the waves' sums.
+// more for the waves' sums.  The groups are counted as if their offsets were
+// `ordered` and, where a wave finds some that are not (-1 in its sum's place),
+// once more.  bounds, if any: begin | end << 16 of every group.
 template <int WAVES>
-__device__ __forceinline__ int mx_tiles_before(const MxArgs &g, int high, int32_t *cum)
+__device__ __forceinline__ int mx_tiles_before(const MxArgs &g, int high, int32_t *cum, uint32_t *bounds, bool &ordered)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int32_t *part = cum + g.E + 1;
     const int P = (g.E + 64 * WAVES - 1) / (64 * WAVES);
-    int sum = 0;
-    for (int i = 0; i < P; ++i) {
-        int b = 0, f = 0;
-        if (tid * P + i < g.E) mx_group(g, tid * P + i, b, f);
-        sum += (f - b + high - 1) / high;
-    }
-    int run = sum;
+    int before = 0;
+    for (ordered = true;; ordered = false) {
+        int sum = 0;
+        bool fell = false;
+        for (int i = 0; i < P; ++i) {
+            int b = 0, f = 0;
+            if (tid * P + i < g.E) fell |= !mx_group(g, tid * P + i, ordered, b, f);
+            sum += (f - b + high - 1) / high;
+        }
+        int run = sum;
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int o = __shfl_up(run, d);
-        if (lane >= d) run += o;
+        for (int d = 1; d < 64; d *= 2) {
+            const int o = __shfl_up(run, d);
+            if (lane >= d) run += o;
+        }
+        const bool again = ordered && __ballot(fell) != 0;
+        if (lane == 63) part[wave] = again ? -1 : run;
+        __syncthreads();
+        before = run - sum;
+        bool counted = true;
+        for (int w = 0; w < WAVES; ++w) {
+            counted &= part[w] >= 0;
+            if (w < wave) before += part[w];
+        }
+        if (counted) break;
+        __syncthreads();  // every wave has read the sums
     }
-    if (lane == 63) part[wave] = run;
-    __syncthreads();
-    int before = run - sum;
-    for (int w = 0; w < wave; ++w) before += part[w];
     for (int i = 0; i < P; ++i) {
         const int e = tid * P + i;
         if (e >= g.E) break;
         int b, f;
-        mx_group(g, e, b, f);
+        mx_group(g, e, ordered, b, f);
         cum[e] = before;
+        if (bounds != nullptr) bounds[e] = (uint32_t)b | (uint32_t)f << 16;
         before += (f - b + high - 1) / high;
         if (e == g.E - 1) cum[g.E] = before;
     }
@@ -128,17 +145,21 @@ __device__ __forceinline__ int mx_tiles_before(const MxArgs &g, int high, int32_
 struct MxGroups {
     int begin = 0, end = 0, before = 0, total = 0;  // lane e: group e
     const int32_t *cum = nullptr;
+    const uint32_t *bounds = nullptr;  // in LDS, where a kernel has room for them
+    bool ordered = true;
 
     template <int WAVES>
-    __device__ __forceinline__ void init(const MxArgs &g, int high, int32_t *table)
+    __device__ __forceinline__ void init(const MxArgs &g, int high, int32_t *table, uint32_t *room = nullptr)
     {
         const int lane = threadIdx.x & 63;
         cum = table;
+        bounds = room;
         if (g.E > 64) {
-            total = mx_tiles_before<WAVES>(g, high, table);
+            total = mx_tiles_before<WAVES>(g, high, table, room, ordered);
             return;
         }
-        if (lane < g.E) mx_group(g, lane, begin, end);
+        const bool fell = lane < g.E && !mx_group(g, lane, true, begin, end);
+        if (__ballot(fell) != 0 && lane < g.E) mx_group(g, lane, false, begin, end);
         const int own = (end - begin + high - 1) / high;
         int run = own;
 #pragma unroll
@@ -150,8 +171,8 @@ struct MxGroups {
         total = __builtin_amdgcn_readlane(run, 63);
     }
     // The group that row tile rt belongs to, the last that begins at or before
-    // it: its rows [b, f) and the tiles before it.  `bounds`: begin | end << 16 in LDS.
-    __device__ __forceinline__ int of(const MxArgs &g, int rt, int &b, int &f, int &first, const uint32_t *bounds = nullptr) const
+    // it: its rows [b, f) and the tiles before it.
+    __device__ __forceinline__ int of(const MxArgs &g, int rt, int &b, int &f, int &first) const
     {
         const int lane = threadIdx.x & 63;
         int n = 0;
@@ -164,7 +185,7 @@ struct MxGroups {
                 b = (int)(bound & 0xFFFFu);
                 f = (int)(bound >> 16);
             } else {
-                mx_group(g, e, b, f);
+                mx_group(g, e, ordered, b, f);
                 b = __builtin_amdgcn_readfirstlane(b);
                 f = __builtin_amdgcn_readfirstlane(f);
             }
@@ -917,13 +938,7 @@ __global__ __launch_bounds__(64 * kMxNarrowWaves) void gemm_mxfp4_narrow_kernel(
     if (GROUPED) {
         if (g.rows != nullptr)
             for (int i = threadIdx.x; i < g.R; i += 64 * kMxNarrowWaves) index[i] = g.rows[i];
-        if (g.E > 64)
-            for (int i = threadIdx.x; i < g.E; i += 64 * kMxNarrowWaves) {
-                int begin, end;
-                mx_group(g, i, begin, end);
-                bounds[i] = (uint32_t)begin | (uint32_t)end << 16;
-            }
-        groups.init<kMxNarrowWaves>(g, 16, cum);
+        groups.init<kMxNarrowWaves>(g, 16, cum, bounds);
         items = groups.total * strips;
         __syncthreads();  // the indices
     }
@@ -952,7 +967,7 @@ __global__ __launch_bounds__(64 * kMxNarrowWaves) void gemm_mxfp4_narrow_kernel(
         it.strip = id;
         if (GROUPED && id < items) {
             int begin, end, first;
-            const int e = groups.of(g, id / strips, begin, end, first, bounds);
+            const int e = groups.of(g, id / strips, begin, end, first);
             const int tiles = (end - begin + 15) / 16, in_group = id - first * strips;
             // a strip's row tiles one after another: its later reads come from the caches
             it.strip = e * strips + in_group / tiles;
