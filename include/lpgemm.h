@@ -415,7 +415,7 @@ lpgemm_status lpgemm_unpack_int4(const uint8_t *packed, int8_t *logical, int64_t
  * an infinity gets s = 255 and zero codes: all its values become NaN.
  * LPGEMM_ERR_INVALID_ARG for negative sizes, another x_dtype, ldx < K with
  * several rows, a null or misaligned pointer; LPGEMM_ERR_UNSUPPORTED for K
- * above LPGEMM_MXFP4_MAX_K.
+ * above LPGEMM_MXFP4_MAX_K or more code bytes than any device holds.
  */
 lpgemm_status lpgemm_mxfp4_quantize(const void *X, lpgemm_out_dtype x_dtype, int64_t ldx, uint8_t *codes,
                                     uint8_t *scales, int64_t rows, int64_t K, hipStream_t stream);

@@ -52,18 +52,35 @@ constexpr int64_t kManyItems = 4 * 256 * 4 * 256;
 // MB, from the cache) 24.7 kept, 28.6 passed by.
 constexpr int64_t kPastCaches = 192 << 20;
 
+// A launch has fewer than 2^32 threads, of 256 to a workgroup: launch(first,
+// count, blocks) for the rows in ranges that one holds (2^30 - 64 rows of up to
+// 128 values).
+template <typename Launch>
+lpgemm_status launch_rows(int64_t rows, int64_t items, int64_t block_items, Launch launch)
+{
+    constexpr int64_t kMostBlocks = (1 << 24) - 1;
+    if (rows * items > INT32_MAX * block_items) return LPGEMM_ERR_UNSUPPORTED;
+    const int64_t most = kMostBlocks * block_items / items;
+    for (int64_t first = 0; first < rows; first += most) {
+        const int64_t count = std::min(most, rows - first);
+        launch(first, count, dim3((unsigned)ceil_div(count * items, block_items)));
+        const lpgemm_status st = launched();
+        if (st != LPGEMM_OK) return st;
+    }
+    return LPGEMM_OK;
+}
+
 template <int IN>
 lpgemm_status launch_quantize(const void *x, int64_t ldx, uint8_t *codes, uint8_t *scales, int64_t rows, int64_t K, hipStream_t stream)
 {
     const int64_t items = ceil_div(K, kMxUnit) * (kMxUnit / 8), total = rows * items;
     const bool many = total >= kManyItems;
-    const int64_t blocks = ceil_div(total, many ? 1024 : 256);
-    if (blocks > INT32_MAX) return LPGEMM_ERR_UNSUPPORTED;
     const bool past = rows * K * (int64_t)element_bytes(IN) > kPastCaches;
     const auto kernel = past ? &mxfp4_quantize_kernel<IN, 4, true> : many ? &mxfp4_quantize_kernel<IN, 4, false> : &mxfp4_quantize_kernel<IN, 1, false>;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, stream, x, ldx, reinterpret_cast<uint32_t *>(codes), scales, rows,
-                       (int32_t)K, (uint32_t)items);
-    return launched();
+    return launch_rows(rows, items, many ? 1024 : 256, [&](int64_t first, int64_t count, dim3 blocks) {
+        hipLaunchKernelGGL(kernel, blocks, dim3(256), 0, stream, static_cast<const uint8_t *>(x) + first * ldx * (int64_t)element_bytes(IN), ldx,
+                           reinterpret_cast<uint32_t *>(codes) + first * items, scales + first * (items / 4), count, (int32_t)K, (uint32_t)items);
+    });
 }
 
 template <int OUT>
@@ -71,14 +88,14 @@ lpgemm_status launch_dequantize(const uint8_t *codes, const uint8_t *scales, voi
 {
     const int64_t items = ceil_div(K, kMxUnit) * (kMxUnit / 8), total = rows * items;
     const bool many = total >= kManyItems;
-    const int64_t blocks = ceil_div(total, many ? 1024 : 256);
-    if (blocks > INT32_MAX) return LPGEMM_ERR_UNSUPPORTED;
     // half as large results too: they are written, so the cache has to put them out
     const bool past = 2 * rows * K * (int64_t)element_bytes(OUT) > kPastCaches;
     const auto kernel = past ? &mxfp4_dequantize_kernel<OUT, 4, true> : many ? &mxfp4_dequantize_kernel<OUT, 4, false> : &mxfp4_dequantize_kernel<OUT, 1, false>;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, stream, reinterpret_cast<const uint32_t *>(codes), scales, y, rows,
-                       (int32_t)K, (uint32_t)items);
-    return launched();
+    return launch_rows(rows, items, many ? 1024 : 256, [&](int64_t first, int64_t count, dim3 blocks) {
+        hipLaunchKernelGGL(kernel, blocks, dim3(256), 0, stream, reinterpret_cast<const uint32_t *>(codes) + first * items,
+                           scales + first * (items / 4), static_cast<uint8_t *>(y) + first * K * (int64_t)element_bytes(OUT), count, (int32_t)K,
+                           (uint32_t)items);
+    });
 }
 
 constexpr int kMaxDevices = 64;
