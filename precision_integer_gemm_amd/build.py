@@ -4,9 +4,11 @@
 
 compiles csrc/lpgemm_api.hip (which includes every integer and fp8 kernel) and
 csrc/mxfp4_api.hip (the microscaled 4-bit kernels) with hipcc into
-precision_integer_gemm_amd/_lpgemm.so, next to this file, csrc/tensor_calls.cpp
-into the Python module _tensor_calls.so, and the measurement probe
-csrc/ceiling_probe.hip into _ceiling.so (loaded only by bench.py).
+precision_integer_gemm_amd/_lpgemm.so, next to this file, and the measurement
+probe csrc/ceiling_probe.hip into _ceiling.so (loaded only by bench.py).  These
+need hipcc alone.  Where PyTorch for ROCm, Python's headers and g++ are there,
+csrc/tensor_calls.cpp becomes the Python module _tensor_calls.so, the short way
+of the microscaled tensor calls; without it they take their longer way.
 """
 from __future__ import annotations
 
@@ -48,6 +50,20 @@ def command(out: str, src: str, *mode: str) -> list[str]:
     ]
 
 
+def calls_missing() -> str | None:
+    """What the Python module of the tensor calls cannot be built without and is not there."""
+    import sysconfig
+    try:
+        import torch
+    except ImportError:
+        return "PyTorch"
+    if torch.version.hip is None:
+        return "PyTorch for ROCm"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    return None if shutil.which("g++") else "g++"
+
+
 def calls_commands(obj: str, out: str) -> tuple[list[str], list[str]]:
     """Compile and link commands of the Python module of the tensor calls: host
     code against PyTorch's headers, linked to the library beside it."""
@@ -81,20 +97,28 @@ def run(cmd: list[str], what: str, verbose: bool) -> None:
 def build(verbose: bool = False) -> str:
     objects = [LIB + "." + os.path.basename(src) + ".o" for src in (SRC, MX_SRC)]
     jobs = [(command(o, src, "-c"), os.path.basename(src)) for o, src in zip(objects, (SRC, MX_SRC))]
-    calls_obj = CALLS_LIB + ".o"
-    calls_compile, calls_link = calls_commands(calls_obj, CALLS_LIB + ".tmp")
-    jobs.append((calls_compile, os.path.basename(CALLS_SRC)))
     jobs.append((command(PROBE_LIB + ".tmp", PROBE_SRC, "-shared"), os.path.basename(PROBE_SRC)))
-    with ThreadPoolExecutor(len(jobs)) as pool:
+    missing, calls_obj = calls_missing(), CALLS_LIB + ".o"
+    with ThreadPoolExecutor(len(jobs) + 1) as pool:
+        if missing is None:
+            calls_compile, calls_link = calls_commands(calls_obj, CALLS_LIB + ".tmp")
+            calls = pool.submit(run, calls_compile, os.path.basename(CALLS_SRC), verbose)
         for done in [pool.submit(run, cmd, what, verbose) for cmd, what in jobs]:
             done.result()
     run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", LIB + ".tmp", *objects], "the library", verbose)
     os.replace(PROBE_LIB + ".tmp", PROBE_LIB)
     os.replace(LIB + ".tmp", LIB)
+    for o in objects:
+        os.remove(o)
+    if missing is not None:
+        if os.path.exists(CALLS_LIB):  # of another library
+            os.remove(CALLS_LIB)
+        print(f"{os.path.basename(CALLS_LIB)} is not built ({missing} is missing): the microscaled tensor calls take their longer way")
+        return LIB
+    calls.result()
     run(calls_link, "the tensor calls", verbose)
     os.replace(CALLS_LIB + ".tmp", CALLS_LIB)
-    for o in (*objects, calls_obj):
-        os.remove(o)
+    os.remove(calls_obj)
     return LIB
 
 
