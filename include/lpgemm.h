@@ -492,9 +492,10 @@ typedef enum lpgemm_kernel LPGEMM_ENUM_BASE {
                                  /* 256 x 256 tiles on the FP6 matrix cores       */
 } lpgemm_kernel;
 /* The mxfp4 products have TILED, TILED_64, TILED_128, TILED_256 (tiles of up to
- * that many rows and columns) and SKINNY (product: K <= 16384, up to 4096 rows;
- * grouped: up to 896 rows of D and 512 groups); anything else forced on them is
- * LPGEMM_ERR_UNSUPPORTED. */
+ * that many rows and columns; TILED_256 with K <= 384 runs as TILED_128, whose
+ * ring takes rows of fewer than four units) and SKINNY (product: K <= 16384, up
+ * to 4096 rows; grouped: up to 896 rows of D and 512 groups); anything else
+ * forced on them is LPGEMM_ERR_UNSUPPORTED. */
 /* LPGEMM_KERNEL_AUTO picks FP6 for int4 x int4 when the fast path applies,
  * the call's workspace holds the re-encoded operands, M > 128, and either the
  * 256 x 256 output tiles number at least twice the compute units with
@@ -540,6 +541,14 @@ typedef struct lpgemm_plan_info {
 lpgemm_status lpgemm_plan(lpgemm_variant variant, const void *A, const void *B, const void *C,
                           int64_t M, int64_t N, int64_t K, size_t workspace_bytes,
                           int32_t cu_count, lpgemm_plan_info *info);
+
+/*
+ * The same for an mxfp4 product of R rows: E == 0 lpgemm_mxfp4, E > 0
+ * lpgemm_mxfp4_grouped with E groups and R rows of A and D.  info->kernel is TILED or
+ * SKINNY, tile_m the most rows of a tile, k_split the waves (SKINNY) or halves
+ * of a workgroup that split K.
+ */
+lpgemm_status lpgemm_mxfp4_plan(int64_t R, int64_t N, int64_t K, int64_t E, int32_t cu_count, lpgemm_plan_info *info);
 
 /*
  * Force a kernel for the later calls made on the calling thread

@@ -17,6 +17,7 @@ from ._binding import (  # noqa: F401
     OK, OUT_BF16, OUT_F16, OUT_F32, OUT_FP8_E4M3, OUT_FP8_E5M2, VARIANT_I4I4, VARIANT_W4A8, LpgemmError, lib,
     lpgemm_fp8_e4m3, lpgemm_fp8_e5m2, lpgemm_int4_int4, lpgemm_int4_int4_blockscaled, lpgemm_int4_int4_scaled, lpgemm_pack_int4, lpgemm_plan,
     lpgemm_set_kernel_override, lpgemm_status_string, lpgemm_unpack_int4, lpgemm_w4a8,
-    lpgemm_mxfp4, lpgemm_mxfp4_dequantize, lpgemm_mxfp4_grouped, lpgemm_mxfp4_quantize, lpgemm_mxfp4_workspace_size,
+    lpgemm_mxfp4, lpgemm_mxfp4_dequantize, lpgemm_mxfp4_grouped, lpgemm_mxfp4_plan, lpgemm_mxfp4_quantize,
+    lpgemm_mxfp4_workspace_size,
     MXFP4_MAX_GROUPS, MXFP4_MAX_K, MXFP4_UNIT, MXFP4_UNIT_CODES, MXFP4_UNIT_SCALES,
     lpgemm_w4a8_blockscaled, lpgemm_w4a8_scaled, lpgemm_workspace_size, SIZE_MAX, STATIC_SCRATCH_BYTES, WORKSPACE_ALIGN)

@@ -34,7 +34,7 @@ EXPORTS = ("lpgemm_int4_int4", "lpgemm_w4a8", "lpgemm_int4_int4_ws", "lpgemm_w4a
            "lpgemm_fp8_e4m3", "lpgemm_fp8_e5m2", "lpgemm_pack_int4",
            "lpgemm_unpack_int4", "lpgemm_status_string", "lpgemm_plan",
            "lpgemm_set_kernel_override", "lpgemm_mxfp4_quantize", "lpgemm_mxfp4_dequantize",
-           "lpgemm_mxfp4", "lpgemm_mxfp4_workspace_size", "lpgemm_mxfp4_grouped")
+           "lpgemm_mxfp4", "lpgemm_mxfp4_workspace_size", "lpgemm_mxfp4_grouped", "lpgemm_mxfp4_plan")
 SIZE_MAX = 2 ** 64 - 1
 STATIC_SCRATCH_BYTES = 128 << 20  # LPGEMM_STATIC_SCRATCH_BYTES
 WORKSPACE_ALIGN = 256
@@ -123,6 +123,8 @@ def lib() -> ctypes.CDLL:
     L.lpgemm_status_string.restype = ctypes.c_char_p
     L.lpgemm_plan.argtypes = [ctypes.c_int, p, p, p, i64, i64, i64, sz, i32, ctypes.POINTER(PlanInfo)]
     L.lpgemm_plan.restype = ctypes.c_int
+    L.lpgemm_mxfp4_plan.argtypes = [i64, i64, i64, i64, i32, ctypes.POINTER(PlanInfo)]
+    L.lpgemm_mxfp4_plan.restype = ctypes.c_int
     L.lpgemm_set_kernel_override.argtypes = [ctypes.c_int]
     L.lpgemm_set_kernel_override.restype = ctypes.c_int
     _lib = L
@@ -147,6 +149,14 @@ def lpgemm_plan(variant: int, M: int, N: int, K: int, A: int = 256, B: int = 256
     ws = SIZE_MAX if workspace_bytes is None else int(workspace_bytes)
     _raise(lib().lpgemm_plan(variant, A, B, C, M, N, K, ws, cu_count, ctypes.byref(info)),
            "lpgemm_plan")
+    return info.as_dict()
+
+
+def lpgemm_mxfp4_plan(R: int, N: int, K: int, E: int = 0, cu_count: int = 0) -> dict:
+    """Kernel and launch shape of an mxfp4 product of R rows (E groups: of a
+    grouped one with R rows of D), host only."""
+    info = PlanInfo()
+    _raise(lib().lpgemm_mxfp4_plan(R, N, K, E, cu_count, ctypes.byref(info)), "lpgemm_mxfp4_plan")
     return info.as_dict()
 
 

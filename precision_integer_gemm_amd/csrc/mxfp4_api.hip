@@ -114,7 +114,7 @@ lpgemm_status allow_lds(Kernel kernel, int bytes, std::once_flag *once, hipError
 }
 
 template <int HM, int FN, int STAGES, int KG, int OUT>
-lpgemm_status launch_tiled(const MxArgs &g, hipStream_t stream)
+lpgemm_status launch_tiled(const MxArgs &g, int64_t blocks, hipStream_t stream)
 {
     using T = MxTile<HM, FN, STAGES>;
     static std::once_flag once[kMaxDevices];
@@ -122,42 +122,19 @@ lpgemm_status launch_tiled(const MxArgs &g, hipStream_t stream)
     const auto kernel = &gemm_mxfp4_tiled_kernel<HM, FN, STAGES, KG, OUT>;
     const lpgemm_status st = allow_lds(kernel, T::lds(LPGEMM_MXFP4_MAX_GROUPS, KG), once, err);
     if (st != LPGEMM_OK) return st;
-    const int tiles_n = (int)ceil_div(g.N, 64 * FN);
-    // at most one ragged row tile a group more than the rows fill
-    const int64_t most = (ceil_div(g.R, 64 * HM) + (g.offsets ? std::min(g.E, g.R) : 0)) * tiles_n;
-    const unsigned blocks = (unsigned)std::min<int64_t>(most, (T::lds(g.E, KG) > 80 * 1024 ? 1 : 2) * (int64_t)compute_units());
-    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256 * KG), T::lds(g.E, KG), stream, g, tiles_n, kXcds);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256 * KG), T::lds(g.E, KG), stream, g, (int)ceil_div(g.N, 64 * FN), kXcds);
     return launched();
 }
 
 template <int OUT>
-lpgemm_status launch_large(const MxArgs &g, hipStream_t stream)
+lpgemm_status launch_large(const MxArgs &g, int64_t blocks, hipStream_t stream)
 {
     static std::once_flag once[kMaxDevices];
     static hipError_t err[kMaxDevices];
     const auto kernel = &gemm_mxfp4_large_kernel<OUT>;
     const lpgemm_status st = allow_lds(kernel, MxLarge::lds(LPGEMM_MXFP4_MAX_GROUPS), once, err);
     if (st != LPGEMM_OK) return st;
-    const int tiles_n = (int)ceil_div(g.N, 256);
-    const int64_t most = (ceil_div(g.R, 256) + (g.offsets ? std::min(g.E, g.R) : 0)) * tiles_n;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(most, compute_units())), dim3(256), MxLarge::lds(g.E), stream, g, tiles_n,
-                       kXcds);
-    return launched();
-}
-
-template <int FA, int S, bool GROUPED, int OUT>
-lpgemm_status launch_narrow(const MxArgs &g, int kw, int stages, hipStream_t stream)
-{
-    using C = MxNarrow<GROUPED>;
-    static std::once_flag once[kMaxDevices];
-    static hipError_t err[kMaxDevices];
-    const auto kernel = &gemm_mxfp4_narrow_kernel<FA, S, GROUPED, OUT>;
-    const lpgemm_status st = allow_lds(kernel, C::lds(kMxNarrowGroups), once, err);
-    if (st != LPGEMM_OK) return st;
-    const int64_t items = ceil_div(g.N, 16) * (GROUPED ? ceil_div(g.R, 16) + std::min(g.E, g.R) : 1);
-    const int64_t tiles = GROUPED ? 1 : ceil_div(g.R, 16 * FA);  // of rows; workgroups of each
-    const int64_t blocks = std::min(ceil_div(items, kMxNarrowWaves / kw), std::max<int64_t>(1, compute_units() / tiles));
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks, (unsigned)tiles), dim3(64 * kMxNarrowWaves), C::lds(g.E), stream, g, kw, stages);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), MxLarge::lds(g.E), stream, g, (int)ceil_div(g.N, 256), kXcds);
     return launched();
 }
 
@@ -173,10 +150,12 @@ bool narrow_serves(const MxArgs &g)
     return g.R <= kNarrowMaxRows && g.U <= 4 * kMxNarrowWaves * kNarrowStages && g.N <= INT32_MAX / 32;
 }
 
-// How the narrow kernel would run: waves to a strip, stages of each, time in us.
+// How the narrow kernel would run: waves to a strip, stages of each, time in
+// us; workgroups, and row tiles of the grid.
 struct NarrowPlan {
     int kw, stages;
     double time;
+    int64_t blocks, tiles;
 };
 // A strip costs its stages and 1.2 more for its sums and what leads to it, so
 // fewer waves for many strips, more where a wave has one.  MI355X, 24 groups of
@@ -187,30 +166,44 @@ NarrowPlan plan_narrow(const MxArgs &g, int64_t cu)
     const bool grouped = g.offsets != nullptr;
     const int64_t strips = ceil_div(g.N, 16) * (grouped ? std::min(g.E, g.R) : 1);
     const int64_t per_tile = grouped ? cu : std::max<int64_t>(1, cu / ceil_div(g.R, g.R <= 16 ? 16 : 32));  // workgroups
-    NarrowPlan best{kMxNarrowWaves, 1, 0};
+    NarrowPlan best{kMxNarrowWaves, 1, 0, 0, 0};
     for (int w = kMxNarrowWaves; w > 0; w /= 2) {
         int64_t s = std::max<int64_t>(1, ceil_div(g.U, 4 * w));
         if (!grouped && s > kNarrowStages) continue;
         if (!grouped && s == 3) s = 4;  // registers for 1, 2 or 4
         const double t = 1.35 * (double)ceil_div(strips, per_tile * (kMxNarrowWaves / w)) * ((double)s + 1.2);
-        if (best.time == 0 || t < best.time) best = {w, (int)s, t};
+        if (best.time == 0 || t < best.time) best = {w, (int)s, t, 0, 0};
     }
+    const int64_t items = ceil_div(g.N, 16) * (grouped ? ceil_div(g.R, 16) + std::min(g.E, g.R) : 1);
+    best.tiles = grouped ? 1 : ceil_div(g.R, g.R <= 16 ? 16 : 32);
+    best.blocks = std::min(ceil_div(items, kMxNarrowWaves / best.kw), std::max<int64_t>(1, cu / best.tiles));
     return best;
 }
 
-template <int OUT>
-lpgemm_status launch_narrow_any(const MxArgs &g, hipStream_t stream)
+template <int FA, int S, bool GROUPED, int OUT>
+lpgemm_status launch_narrow(const MxArgs &g, const NarrowPlan &p, hipStream_t stream)
 {
-    const NarrowPlan p = plan_narrow(g, compute_units());
-    const int kw = p.kw, stages = p.stages;
-    if (g.offsets != nullptr) return launch_narrow<1, 1, true, OUT>(g, kw, stages, stream);
+    using C = MxNarrow<GROUPED>;
+    static std::once_flag once[kMaxDevices];
+    static hipError_t err[kMaxDevices];
+    const auto kernel = &gemm_mxfp4_narrow_kernel<FA, S, GROUPED, OUT>;
+    const lpgemm_status st = allow_lds(kernel, C::lds(kMxNarrowGroups), once, err);
+    if (st != LPGEMM_OK) return st;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)p.blocks, (unsigned)p.tiles), dim3(64 * kMxNarrowWaves), C::lds(g.E), stream, g, p.kw, p.stages);
+    return launched();
+}
+
+template <int OUT>
+lpgemm_status launch_narrow_any(const MxArgs &g, const NarrowPlan &p, hipStream_t stream)
+{
+    if (g.offsets != nullptr) return launch_narrow<1, 1, true, OUT>(g, p, stream);
     if (g.R <= 16)
-        return stages == 1   ? launch_narrow<1, 1, false, OUT>(g, kw, 1, stream)
-               : stages == 2 ? launch_narrow<1, 2, false, OUT>(g, kw, 2, stream)
-                             : launch_narrow<1, 4, false, OUT>(g, kw, 4, stream);
-    return stages == 1   ? launch_narrow<2, 1, false, OUT>(g, kw, 1, stream)
-           : stages == 2 ? launch_narrow<2, 2, false, OUT>(g, kw, 2, stream)
-                         : launch_narrow<2, 4, false, OUT>(g, kw, 4, stream);
+        return p.stages == 1   ? launch_narrow<1, 1, false, OUT>(g, p, stream)
+               : p.stages == 2 ? launch_narrow<1, 2, false, OUT>(g, p, stream)
+                               : launch_narrow<1, 4, false, OUT>(g, p, stream);
+    return p.stages == 1   ? launch_narrow<2, 1, false, OUT>(g, p, stream)
+           : p.stages == 2 ? launch_narrow<2, 2, false, OUT>(g, p, stream)
+                           : launch_narrow<2, 4, false, OUT>(g, p, stream);
 }
 
 // The tiled kernels' shapes and what one of their tiles costs in time: us for
@@ -268,22 +261,6 @@ int choose_shape(const MxArgs &g, int64_t cu, double *time)
     return best;
 }
 
-template <int OUT>
-lpgemm_status launch_shape(const MxArgs &g, int shape, hipStream_t stream)
-{
-    // 32-bit tile counts
-    const Shape &s = kShapes[shape];
-    if (ceil_div(g.R, s.high) + g.E > INT32_MAX / ceil_div(g.N, s.wide)) return LPGEMM_ERR_UNSUPPORTED;
-    switch (shape) {
-    case kShape64: return launch_tiled<1, 1, 4, 1, OUT>(g, stream);
-    case kShape64Split: return launch_tiled<1, 1, 4, 2, OUT>(g, stream);
-    case kShape64x128: return launch_tiled<1, 2, 2, 1, OUT>(g, stream);
-    case kShape128: return launch_tiled<2, 2, 2, 1, OUT>(g, stream);
-    case kShape128Deep: return launch_tiled<2, 2, 4, 1, OUT>(g, stream);
-    default: return g.U >= MxLarge::kMinUnits ? launch_large<OUT>(g, stream) : launch_tiled<2, 2, 2, 1, OUT>(g, stream);
-    }
-}
-
 // Whether the narrow kernel takes a call that it can serve.  Few rows are its
 // own (grouped: up to eight a group on average); beyond, it wins where the tiles
 // are few and K long, as its waves split K (us, 64 x 64 tiles / narrow):
@@ -300,23 +277,68 @@ bool narrow_pays(const MxArgs &g, int64_t cu, double tiled)
     return g.R <= kNarrowRows || plan_narrow(g, cu).time + 0.5 < tiled;
 }
 
-template <int OUT>
-lpgemm_status launch_product(const MxArgs &g, hipStream_t stream)
+// What runs a product: the narrow kernel, or a shape of the tiled ones on so
+// many workgroups of so many threads.
+struct MxPlan {
+    int shape;  // kShapeCount: narrow
+    NarrowPlan narrow;
+    int64_t blocks;
+    int threads;
+};
+
+lpgemm_status plan_shape(const MxArgs &g, int shape, int64_t cu, MxPlan *p)
 {
-    const int64_t cu = compute_units();
-    const int forced = forced_kernel();
+    const Shape &s = kShapes[shape];
+    const int64_t tiles_n = ceil_div(g.N, s.wide);
+    // 32-bit tile counts; at most one ragged row tile a group more than the rows fill
+    if (ceil_div(g.R, s.high) + g.E > INT32_MAX / tiles_n) return LPGEMM_ERR_UNSUPPORTED;
+    const int64_t most = (ceil_div(g.R, s.high) + (g.offsets ? std::min(g.E, g.R) : 0)) * tiles_n;
+    const int lds = shape == kShape64         ? MxTile<1, 1, 4>::lds(g.E, 1)
+                    : shape == kShape64Split  ? MxTile<1, 1, 4>::lds(g.E, 2)
+                    : shape == kShape64x128   ? MxTile<1, 2, 2>::lds(g.E, 1)
+                    : shape == kShape128      ? MxTile<2, 2, 2>::lds(g.E, 1)
+                    : shape == kShape128Deep  ? MxTile<2, 2, 4>::lds(g.E, 1)
+                                              : MxLarge::lds(g.E);
+    *p = MxPlan{shape, {}, std::min(most, (lds > 80 * 1024 ? 1 : 2) * cu), shape == kShape64Split ? 512 : 256};
+    return LPGEMM_OK;
+}
+
+lpgemm_status plan_product(const MxArgs &g, int64_t cu, int forced, MxPlan *p)
+{
+    const auto narrow = [&] {
+        const NarrowPlan n = plan_narrow(g, cu);
+        *p = MxPlan{kShapeCount, n, n.blocks * n.tiles, 64 * kMxNarrowWaves};
+        return LPGEMM_OK;
+    };
     if (forced == LPGEMM_KERNEL_AUTO || forced == LPGEMM_KERNEL_TILED) {
         double time = 0;
         const int shape = choose_shape(g, cu, &time);
-        if (forced == LPGEMM_KERNEL_AUTO && narrow_serves(g) && narrow_pays(g, cu, time)) return launch_narrow_any<OUT>(g, stream);
-        return launch_shape<OUT>(g, shape, stream);
+        if (forced == LPGEMM_KERNEL_AUTO && narrow_serves(g) && narrow_pays(g, cu, time)) return narrow();
+        return plan_shape(g, shape, cu, p);
     }
     switch (forced) {
-    case LPGEMM_KERNEL_TILED_64: return launch_shape<OUT>(g, g.R * (int64_t)g.N > 64 * 64 * cu || g.U < kSplitUnits ? kShape64 : kShape64Split, stream);
-    case LPGEMM_KERNEL_TILED_128: return launch_shape<OUT>(g, g.R * (int64_t)g.N > 128 * 128 * cu ? kShape128 : kShape128Deep, stream);
-    case LPGEMM_KERNEL_TILED_256: return launch_shape<OUT>(g, kShape256, stream);
-    case LPGEMM_KERNEL_SKINNY: return narrow_serves(g) ? launch_narrow_any<OUT>(g, stream) : LPGEMM_ERR_UNSUPPORTED;
+    case LPGEMM_KERNEL_TILED_64: return plan_shape(g, g.R * (int64_t)g.N > 64 * 64 * cu || g.U < kSplitUnits ? kShape64 : kShape64Split, cu, p);
+    case LPGEMM_KERNEL_TILED_128: return plan_shape(g, g.R * (int64_t)g.N > 128 * 128 * cu ? kShape128 : kShape128Deep, cu, p);
+    case LPGEMM_KERNEL_TILED_256: return plan_shape(g, g.U < MxLarge::kMinUnits ? kShape128 : kShape256, cu, p);
+    case LPGEMM_KERNEL_SKINNY: return narrow_serves(g) ? narrow() : LPGEMM_ERR_UNSUPPORTED;
     default: return LPGEMM_ERR_UNSUPPORTED;
+    }
+}
+
+template <int OUT>
+lpgemm_status launch_product(const MxArgs &g, hipStream_t stream)
+{
+    MxPlan p;
+    const lpgemm_status st = plan_product(g, compute_units(), forced_kernel(), &p);
+    if (st != LPGEMM_OK) return st;
+    switch (p.shape) {
+    case kShape64: return launch_tiled<1, 1, 4, 1, OUT>(g, p.blocks, stream);
+    case kShape64Split: return launch_tiled<1, 1, 4, 2, OUT>(g, p.blocks, stream);
+    case kShape64x128: return launch_tiled<1, 2, 2, 1, OUT>(g, p.blocks, stream);
+    case kShape128: return launch_tiled<2, 2, 2, 1, OUT>(g, p.blocks, stream);
+    case kShape128Deep: return launch_tiled<2, 2, 4, 1, OUT>(g, p.blocks, stream);
+    case kShape256: return launch_large<OUT>(g, p.blocks, stream);
+    default: return launch_narrow_any<OUT>(g, p.narrow, stream);
     }
 }
 
@@ -397,6 +419,30 @@ lpgemm_status lpgemm_mxfp4_workspace_size(int64_t M, int64_t N, int64_t K, int32
     if (bytes == nullptr || M < 0 || N < 0 || K < 0) return LPGEMM_ERR_INVALID_ARG;
     *bytes = 0;
     if (K > LPGEMM_MXFP4_MAX_K || M > LPGEMM_MXFP4_MAX_ROWS || N > LPGEMM_MXFP4_MAX_ROWS) return LPGEMM_ERR_UNSUPPORTED;
+    return LPGEMM_OK;
+}
+
+lpgemm_status lpgemm_mxfp4_plan(int64_t R, int64_t N, int64_t K, int64_t E, int32_t cu_count, lpgemm_plan_info *info)
+{
+    if (info == nullptr || R < 0 || N < 0 || K < 0 || E < 0) return LPGEMM_ERR_INVALID_ARG;
+    if (K > LPGEMM_MXFP4_MAX_K || R > LPGEMM_MXFP4_MAX_ROWS || N > LPGEMM_MXFP4_MAX_ROWS || E > LPGEMM_MXFP4_MAX_GROUPS)
+        return LPGEMM_ERR_UNSUPPORTED;
+    *info = lpgemm_plan_info{};
+    if (R == 0 || N == 0) return LPGEMM_OK;
+    static const int32_t some = 0;  // offsets are there or not, nobody reads them
+    const MxArgs g{nullptr, nullptr, nullptr, nullptr, nullptr, E > 0 ? &some : nullptr, nullptr,
+                   (int32_t)R, (int32_t)R, (int32_t)N, (int32_t)ceil_div(K, kMxUnit), (int32_t)std::max<int64_t>(E, 1)};
+    MxPlan p;
+    const lpgemm_status st = plan_product(g, cu_count > 0 ? cu_count : 256, forced_kernel(), &p);
+    if (st != LPGEMM_OK) return st;
+    const bool narrow = p.shape == kShapeCount;
+    info->kernel = narrow ? LPGEMM_KERNEL_SKINNY : LPGEMM_KERNEL_TILED;
+    info->tile_m = !narrow ? kShapes[p.shape].high : E > 0 || R <= 16 ? 16 : 32;
+    info->tile_n = narrow ? 16 : kShapes[p.shape].wide;
+    info->k_split = narrow ? p.narrow.kw : p.shape == kShape64Split ? 2 : 1;
+    info->workgroups = p.blocks;
+    info->threads = p.threads;
+    info->k_chunks = 1;
     return LPGEMM_OK;
 }
 
