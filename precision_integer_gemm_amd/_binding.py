@@ -647,7 +647,8 @@ def lpgemm_mxfp4_workspace_size(M: int, N: int, K: int, cu_count: int = 0) -> in
 def lpgemm_mxfp4(A, SFA, B, SFB, *, dtype=None, out=None, workspace="auto", stream=None):
     """D[M,N] = A . B^T of mxfp4 operands (codes [M, 64 U] and [N, 64 U], scales
     [M, 4 U] and [N, 4 U]) with fp32 accumulation, as bfloat16 (default),
-    float16 or float32; workspace as for lpgemm_int4_int4."""
+    float16 or float32.  workspace: "auto", None or a uint8 device tensor, as
+    for lpgemm_int4_int4; no kernel takes scratch memory at present."""
     _mx_torch()
     if out is None and stream is None and isinstance(workspace, str) and workspace == "auto":
         made = _mx[3].product(A, SFA, B, SFB, dtype)
@@ -660,8 +661,7 @@ def lpgemm_mxfp4(A, SFA, B, SFB, *, dtype=None, out=None, workspace="auto", stre
     M, N, K = A.shape[0], B.shape[0], MXFP4_UNIT * units
     D, code = _mx_out(out, dtype, M, N, device)
     if isinstance(workspace, str) and workspace == "auto":
-        n = lpgemm_mxfp4_workspace_size(M, N, K)
-        workspace = _mx[0].empty(n, dtype=_mx[0].uint8, device=device) if n else None
+        workspace = None  # no kernel takes one
     ws, nws, _keep = _workspace(workspace, None, M, N, K, True, device)
     _mx_launch(_mx[1].lpgemm_mxfp4, device.index, stream, A.data_ptr(), SFA.data_ptr(), B.data_ptr(), SFB.data_ptr(),
                D.data_ptr(), code, M, N, K, ws, nws)

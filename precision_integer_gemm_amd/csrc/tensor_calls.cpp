@@ -144,14 +144,9 @@ PyObject *product(PyObject *, PyObject *const *args, Py_ssize_t n)
         !out_type(args[4], &type, &code))
         Py_RETURN_NONE;
     const int64_t M = a.codes->size(0), N = b.codes->size(0), K = kUnit * a.units;
-    size_t size = 0;
-    if (lpgemm_mxfp4_workspace_size(M, N, K, 0, &size) != LPGEMM_OK) Py_RETURN_NONE;
     const at::Tensor d = fresh({M, N}, type, *a.codes);
-    at::Tensor workspace;  // PyTorch's allocations are aligned beyond the 256 bytes that it needs
-    if (size > 0) workspace = fresh({(int64_t)size}, at::kByte, *a.codes);
     if (!launch(device, [&](hipStream_t s) {
-            return lpgemm_mxfp4(bytes(*a.codes), bytes(*a.scales), bytes(*b.codes), bytes(*b.scales), d.data_ptr(), code, M, N, K,
-                                size > 0 ? workspace.data_ptr() : nullptr, size, s);
+            return lpgemm_mxfp4(bytes(*a.codes), bytes(*a.scales), bytes(*b.codes), bytes(*b.scales), d.data_ptr(), code, M, N, K, nullptr, 0, s);
         }))
         Py_RETURN_NONE;
     return THPVariable_Wrap(d);
