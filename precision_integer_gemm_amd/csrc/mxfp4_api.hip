@@ -88,9 +88,13 @@ lpgemm_status launch_dequantize(const uint8_t *codes, const uint8_t *scales, voi
 {
     const int64_t items = ceil_div(K, kMxUnit) * (kMxUnit / 8), total = rows * items;
     const bool many = total >= kManyItems;
-    // half as large results too: they are written, so the cache has to put them out
-    const bool past = 2 * rows * K * (int64_t)element_bytes(OUT) > kPastCaches;
-    const auto kernel = past ? &mxfp4_dequantize_kernel<OUT, 4, true> : many ? &mxfp4_dequantize_kernel<OUT, 4, false> : &mxfp4_dequantize_kernel<OUT, 1, false>;
+    // half as large 16-bit results too: they are written, so the cache has to put
+    // them out.  fp32 results leave in two pieces, each half of every 32 bytes,
+    // which the caches put together: 8192 x 8192 (268 MB) 75.8 us kept, 109 passed
+    // by; in bf16 (134 MB) 31.0 kept, 25.2 passed by
+    constexpr bool kMayPass = OUT != OUT_F32;
+    const bool past = kMayPass && 2 * rows * K * (int64_t)element_bytes(OUT) > kPastCaches;
+    const auto kernel = past ? &mxfp4_dequantize_kernel<OUT, 4, kMayPass> : many ? &mxfp4_dequantize_kernel<OUT, 4, false> : &mxfp4_dequantize_kernel<OUT, 1, false>;
     return launch_rows(rows, items, many ? 1024 : 256, [&](int64_t first, int64_t count, dim3 blocks) {
         hipLaunchKernelGGL(kernel, blocks, dim3(256), 0, stream, reinterpret_cast<const uint32_t *>(codes) + first * items,
                            scales + first * (items / 4), static_cast<uint8_t *>(y) + first * K * (int64_t)element_bytes(OUT), count, (int32_t)K,
