@@ -672,7 +672,9 @@ def lpgemm_mxfp4_grouped(A, SFA, B, SFB, offsets, *, rows=None, dtype=None, out=
     """The product of each group of rows with its own matrix: row i of the result,
     offsets[e] <= i < offsets[e + 1], is row rows[i] of A times B[e]^T (rows
     None: row i; an index outside A's rows stands for zeros).  A codes [T, 64 U],
-    B codes [E, N, 64 U], offsets int32 [E + 1] and rows int32 on the device."""
+    B codes [E, N, 64 U], offsets int32 [E + 1] and rows int32 on the device.
+    Rows that no group holds are not written: without `out` they are whatever
+    the new tensor's memory held."""
     _mx_torch()
     if out is None and stream is None:
         made = _mx[3].grouped(A, SFA, B, SFB, offsets, rows, dtype)

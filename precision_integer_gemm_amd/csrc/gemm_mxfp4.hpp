@@ -9,10 +9,13 @@
 // Three kernels (the choice between them: mxfp4_api.hip):
 //  - tiled, 64 x 64 to 128 x 128 tiles: bound by what a compute unit draws from
 //    its L2 and beyond (60-100 GB/s): 1110 rows on 13 groups of 1001 x 2897
-//    12.8 us, 4096 on 64 of 2048 x 4096 77 us (3.9 TB/s), 333 x 1001 x 2897 7.4 us.
-//  - large, tiles of 256 columns: bound by the matrix cores at the clock they
-//    run at (1.75 GHz, 57% busy on 8192^3): 261 us, 4.2 PFLOP/s; 3000 x 5120 x
-//    6144 51 us, 16384 rows on 32 groups of 4096 x 4096 191 us (2.9 PFLOP/s).
+//    12.7 us, 4096 on 64 of 2048 x 4096 77 us (3.9 TB/s), 333 x 1001 x 2897 7.2 us.
+//  - large, tiles of 256 columns: bound by the one stream of instructions of a
+//    SIMD's one wave, which issues copies, reads and MFMAs, and by a tile's
+//    beginning and end.  8192^3 261 us, 4.2 PFLOP/s, with the matrix cores 57%
+//    busy at 1.74 GHz (the same MFMAs on registers alone: 6.2-6.5 PFLOP/s at
+//    1.59-1.66 GHz); 3000 x 5120 x 6144 50 us; 16384 rows on 32 groups of 4096 x
+//    4096 192-202 us (2.8 PFLOP/s, 35% busy at 2.03 GHz).
 //  - narrow, few rows: bound by memory: 16 x 28672 x 8192 23.9 us (5.3 TB/s), 64
 //    rows on 24 of 32 groups of 4096 x 4096 36 us (6.0 TB/s), 1 x 4096 x 4096
 //    4.3 us on the device.

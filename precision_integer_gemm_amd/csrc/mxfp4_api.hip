@@ -272,9 +272,25 @@ int choose_shape(const MxArgs &g, int64_t cu, double *time)
 //     100 x 100 x 16384     22.9 / 13.1        1000 x 64 x 16384    22.2 / 14.2
 //     64 x 8192 x 8192      13.3 / 18.1        333 x 1001 x 2897     7.5 /  8.5
 // Few rows, best tiles / narrow, weights from memory, as in use: 16 x 28672 x
-// 8192 29.5 / 23.9, 32 x 28672 x 8192 30.3 / 29.4, 16 x 12313 x 7906 15.4 / 14.4,
-// 25 x 12313 x 7906 15.9 / 17.5, 32 x 4096 x 4096 9.1 / 6.2 (weights that the
-// last-level cache holds: 16 x 28672 x 8192 21.2 / 23.0).
+// 8192 29.5 / 23.9, 16 x 12313 x 7906 15.4 / 14.4 (weights that the last-level
+// cache holds: 16 x 28672 x 8192 21.2 / 23.0).  With 17 to 32 rows it wins where
+// its strips fill their rounds, and loses up to 18% where they do not:
+//     17 x 4096 x 4096       7.6 /  5.3        17 x 12313 x 7906    15.5 / 16.7
+//     32 x 4096 x 4096       7.7 /  6.3        25 x 12313 x 7906    15.9 / 17.6
+//     24 x 28672 x 8192     30.3 / 27.8        32 x 12313 x 7906    16.3 / 19.2
+//     32 x 28672 x 8192     30.7 / 29.4        32 x 8192 x 8192     15.4 / 15.8
+//     24 x 4096 x 14336     20.6 / 13.3        32 x 4096 x 14336    21.5 / 14.9
+// (the estimates are of weights in the caches and do not tell these apart).
+// Grouped, the host knows the groups' average alone.  32 groups of 4096 x 4096,
+// best tiles / narrow by rows a group, shared out evenly, by chance (the largest
+// has 6, 22, 55, 69, 107 rows), and all rows in one group:
+//     1    53.8 / 44.4     25.2 / 23.3      9.8 / 12.8
+//     4    54.9 / 45.6     42.6 / 35.0     13.0 / 11.3
+//     8    54.7 / 49.6     43.0 / 46.9     13.6 / 23.3
+//     12   56.1 / 53.9     44.0 / 60.2     14.4 / 35.0
+//     16   55.6 / 57.6     47.4 / 73.1     14.8 / 46.8
+// 64 groups of 2048 x 4096 and 8 of 4096 x 4096 meet in the same places (8 rows:
+// 55.3 / 50.1, 42.8 / 49.0, 13.6 / 23.5; 16.7 / 15.1, 14.6 / 14.5, 10.9 / 12.8).
 bool narrow_pays(const MxArgs &g, int64_t cu, double tiled)
 {
     if (g.offsets != nullptr) return g.R <= 8 * (int64_t)g.E;
