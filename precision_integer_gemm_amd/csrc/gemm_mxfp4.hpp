@@ -9,13 +9,13 @@
 // Three kernels (the choice between them: mxfp4_api.hip):
 //  - tiled, 64 x 64 to 128 x 128 tiles: bound by what a compute unit draws from
 //    its L2 and beyond (60-100 GB/s): 1110 rows on 13 groups of 1001 x 2897
-//    12.7 us, 4096 on 64 of 2048 x 4096 77 us (3.9 TB/s), 333 x 1001 x 2897 7.2 us.
+//    12.4 us, 4096 on 64 of 2048 x 4096 77 us (3.9 TB/s), 333 x 1001 x 2897 7.2 us.
 //  - large, tiles of 256 columns: bound by the one stream of instructions of a
 //    SIMD's one wave, which issues copies, reads and MFMAs, and by a tile's
 //    beginning and end.  8192^3 261 us, 4.2 PFLOP/s, with the matrix cores 57%
 //    busy at 1.74 GHz (the same MFMAs on registers alone: 6.2-6.5 PFLOP/s at
 //    1.59-1.66 GHz); 3000 x 5120 x 6144 50 us; 16384 rows on 32 groups of 4096 x
-//    4096 192-202 us (2.8 PFLOP/s, 35% busy at 2.03 GHz).
+//    4096 190-202 us (2.8 PFLOP/s, 35% busy at 2.03 GHz).
 //  - narrow, few rows: bound by memory: 16 x 28672 x 8192 23.9 us (5.3 TB/s), 64
 //    rows on 24 of 32 groups of 4096 x 4096 36 us (6.0 TB/s), 1 x 4096 x 4096
 //    4.3 us on the device.
@@ -43,10 +43,11 @@ struct MxArgs {
 // no offset is below the one before it; false comes back where e's are not.
 __device__ __forceinline__ bool mx_group(const MxArgs &g, int e, bool ordered, int &begin, int &end)
 {
-    begin = min(max(g.offsets[e], 0), g.R);
-    if (!ordered)
+    const int first = g.offsets[e], after = g.offsets[e + 1];  // both on their way at once
+    const int next = min(max(after, 0), g.R);
+    begin = min(max(first, 0), g.R);
+    if (__builtin_expect(!ordered, 0))
         for (int i = 0; i < e; ++i) begin = max(begin, min(g.offsets[i], g.R));
-    const int next = min(max(g.offsets[e + 1], 0), g.R);
     end = max(begin, next);
     return next >= begin;
 }
@@ -90,6 +91,21 @@ __device__ __forceinline__ uint32_t mx_pack2(float a, float b)
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, mx_f16x2));
 }
 
+// The sum over the lanes up to this one, all 64 active: within rows of 16 lanes,
+// then the rows' last lanes into the rows behind them.  Every instruction before
+// the first copy costs its fetch: 1105 rows on 13 groups of 1001 x 2897 take 10.7
+// us on the device, 11.0 with a permutation through LDS for each of the six steps.
+__device__ __forceinline__ int mx_scan(int x)
+{
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // row_shr:1, 2, 4, 8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // row_bcast:15 to rows 1, 3
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // row_bcast:31 to rows 2, 3
+    return x;
+}
+
 // Row tiles of `high` rows before each group, summed into cum[0 .. E], and
 // their number: thread t takes groups t P .. t P + P - 1.  cum has WAVES words
 // more for the waves' sums.  The groups are counted as if their offsets were
@@ -110,22 +126,19 @@ __device__ __forceinline__ int mx_tiles_before(const MxArgs &g, int high, int32_
             if (tid * P + i < g.E) fell |= !mx_group(g, tid * P + i, ordered, b, f);
             sum += (f - b + high - 1) / high;
         }
-        int run = sum;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int o = __shfl_up(run, d);
-            if (lane >= d) run += o;
-        }
+        const int run = mx_scan(sum);
         const bool again = ordered && __ballot(fell) != 0;
         if (lane == 63) part[wave] = again ? -1 : run;
         __syncthreads();
         before = run - sum;
-        bool counted = true;
+        int all = 0;  // negative: a wave's offsets fall
+#pragma unroll
         for (int w = 0; w < WAVES; ++w) {
-            counted &= part[w] >= 0;
-            if (w < wave) before += part[w];
+            const int p = part[w];
+            all |= p;
+            before += w < wave ? p : 0;
         }
-        if (counted) break;
+        if (__builtin_expect(__builtin_amdgcn_readfirstlane(all) >= 0, 1)) break;
         __syncthreads();  // every wave has read the sums
     }
     for (int i = 0; i < P; ++i) {
@@ -162,14 +175,8 @@ struct MxGroups {
             return;
         }
         const bool fell = lane < g.E && !mx_group(g, lane, true, begin, end);
-        if (__ballot(fell) != 0 && lane < g.E) mx_group(g, lane, false, begin, end);
-        const int own = (end - begin + high - 1) / high;
-        int run = own;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int o = __shfl_up(run, d);
-            if (lane >= d) run += o;
-        }
+        if (__builtin_expect(__ballot(fell) != 0, 0) && lane < g.E) mx_group(g, lane, false, begin, end);
+        const int own = (end - begin + high - 1) / high, run = mx_scan(own);
         before = run - own;
         total = __builtin_amdgcn_readlane(run, 63);
     }
