@@ -7,6 +7,7 @@ is no fallback of any kind, and a missing library is an error.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -34,13 +35,21 @@ EXPORTS = ("lpgemm_int4_int4", "lpgemm_w4a8", "lpgemm_int4_int4_ws", "lpgemm_w4a
            "lpgemm_fp8_e4m3", "lpgemm_fp8_e5m2", "lpgemm_pack_int4",
            "lpgemm_unpack_int4", "lpgemm_status_string", "lpgemm_plan",
            "lpgemm_set_kernel_override", "lpgemm_mxfp4_quantize", "lpgemm_mxfp4_dequantize",
-           "lpgemm_mxfp4", "lpgemm_mxfp4_workspace_size", "lpgemm_mxfp4_grouped", "lpgemm_mxfp4_plan")
+           "lpgemm_mxfp4", "lpgemm_mxfp4_workspace_size", "lpgemm_mxfp4_grouped", "lpgemm_mxfp4_plan",
+           "lpgemm_fp8_block_quantize", "lpgemm_fp8_block_dequantize", "lpgemm_fp8_block",
+           "lpgemm_fp8_block_grouped", "lpgemm_fp8_block_plan", "lpgemm_route", "lpgemm_route_workspace_size",
+           "lpgemm_route_backward", "lpgemm_combine", "lpgemm_combine_backward")
 SIZE_MAX = 2 ** 64 - 1
 STATIC_SCRATCH_BYTES = 128 << 20  # LPGEMM_STATIC_SCRATCH_BYTES
 WORKSPACE_ALIGN = 256
 # microscaled 4-bit rows: units of 128 values, 64 code bytes and 4 scale bytes
 MXFP4_UNIT, MXFP4_UNIT_CODES, MXFP4_UNIT_SCALES = 128, 64, 4
 MXFP4_MAX_K, MXFP4_MAX_GROUPS = 1 << 20, 1024
+# e4m3 rows with a scale per block of 128 values
+FP8_BLOCK, FP8_BLOCK_MAX_K, FP8_BLOCK_MAX_GROUPS = 128, 1 << 20, 1024
+# lpgemm_route_score, and the routing's limits
+ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
+ROUTE_MAX_EXPERTS, ROUTE_MAX_TOP, ROUTE_MAX_GROUPS = 1024, 32, 64
 
 
 class LpgemmError(RuntimeError):
@@ -61,6 +70,16 @@ class PlanInfo(ctypes.Structure):
                 "workgroups": self.workgroups, "threads": self.threads,
                 "k_chunks": self.k_chunks, "workspace_bytes": self.workspace_bytes}
 
+
+class RouteOptions(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("top", ctypes.c_int32), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+# What lpgemm_route gives: experts and weights [T, top]; every expert's rows are
+# offsets[e] .. offsets[e + 1] - 1, row i is token rows[i], and the token's k-th
+# expert has it in row places[t, k].
+Routing = collections.namedtuple("Routing", "experts weights rows offsets places")
 
 _lib = None
 
@@ -118,6 +137,22 @@ def lib() -> ctypes.CDLL:
     L.lpgemm_mxfp4_grouped.argtypes = [p, p, i64, p, p, p, i64, p, p, ctypes.c_int, i64, i64, i64, p]
     for name in ("lpgemm_mxfp4_quantize", "lpgemm_mxfp4_dequantize", "lpgemm_mxfp4",
                  "lpgemm_mxfp4_workspace_size", "lpgemm_mxfp4_grouped"):
+        getattr(L, name).restype = ctypes.c_int
+    L.lpgemm_fp8_block_quantize.argtypes = [p, ctypes.c_int, i64, i64, i32, p, p, i64, i64, p]
+    L.lpgemm_fp8_block_dequantize.argtypes = [p, p, i64, p, ctypes.c_int, i64, i64, p]
+    L.lpgemm_fp8_block.argtypes = [p, p, p, p, i64, p, ctypes.c_int, i64, i64, i64, p]
+    L.lpgemm_fp8_block_grouped.argtypes = [p, p, i64, p, p, p, i64, i64, p, p, ctypes.c_int, i64, i64, i64, p]
+    L.lpgemm_fp8_block_plan.argtypes = [i64, i64, i64, i64, i32, ctypes.POINTER(PlanInfo)]
+    for name in ("lpgemm_fp8_block_quantize", "lpgemm_fp8_block_dequantize", "lpgemm_fp8_block",
+                 "lpgemm_fp8_block_grouped", "lpgemm_fp8_block_plan"):
+        getattr(L, name).restype = ctypes.c_int
+    options = ctypes.POINTER(RouteOptions)
+    L.lpgemm_route.argtypes = [p, ctypes.c_int, i64, p, options, p, p, p, p, p, i64, i64, p, sz, p]
+    L.lpgemm_route_workspace_size.argtypes = [i64, i64, ctypes.POINTER(sz)]
+    L.lpgemm_route_backward.argtypes = [p, p, ctypes.c_int, i64, p, options, p, i64, i64, p]
+    L.lpgemm_combine.argtypes = [p, ctypes.c_int, i64, p, p, p, p, ctypes.c_int, i64, i64, i64, p]
+    L.lpgemm_combine_backward.argtypes = [p, ctypes.c_int, p, ctypes.c_int, i64, p, p, p, p, i64, i64, i64, p]
+    for name in ("lpgemm_route", "lpgemm_route_workspace_size", "lpgemm_route_backward", "lpgemm_combine", "lpgemm_combine_backward"):
         getattr(L, name).restype = ctypes.c_int
     L.lpgemm_status_string.argtypes = [ctypes.c_int]
     L.lpgemm_status_string.restype = ctypes.c_char_p
@@ -698,3 +733,279 @@ def lpgemm_mxfp4_grouped(A, SFA, B, SFB, offsets, *, rows=None, dtype=None, out=
     _mx_launch(_mx[1].lpgemm_mxfp4_grouped, device.index, stream, A.data_ptr(), SFA.data_ptr(), T, index, B.data_ptr(),
                SFB.data_ptr(), E, offsets.data_ptr(), D.data_ptr(), code, R, N, MXFP4_UNIT * units)
     return D
+
+
+# ---- e4m3 with a scale per block of 128 ------------------------------------------
+def _f8_types():
+    torch = _torch()
+    return (torch.float8_e4m3fn, torch.uint8)
+
+
+def _check_f8(codes, scales, name: str, dim: int, device=None):
+    """(units per row, rows that share a scale) of an fp8_block operand."""
+    torch = _torch()
+    _check_on(codes, name, _f8_types(), dim, device)
+    _check_on(scales, f"scales of {name}", (torch.float32,), dim, codes.device)
+    units, rest = divmod(codes.shape[-1], FP8_BLOCK)
+    *lead, rows = codes.shape[:-1]
+    for block_rows in (1, FP8_BLOCK):
+        if not rest and tuple(scales.shape) == (*lead, -(-rows // block_rows), units):
+            return units, block_rows
+    raise ValueError(f"{name} must have shape (..., rows, {FP8_BLOCK} U) and its scales (..., rows or ceil(rows / {FP8_BLOCK}), U), "
+                     f"got {tuple(codes.shape)} and {tuple(scales.shape)}")
+
+
+def lpgemm_fp8_block_quantize(x, *, block_rows=1, power_of_two=False, codes=None, scales=None, stream=None):
+    """Rows of float32, bfloat16 or float16 values [rows, K] -> (codes float8_e4m3fn
+    [rows, 128 U], scales float32 [ceil(rows / block_rows), U]) with U = ceil(K /
+    128): one scale for each block of 128 values of a row (block_rows 1:
+    activations) or of 128 x 128 values (block_rows 128: weights), the block's
+    largest magnitude / 448, or with power_of_two the power of two above that.
+    Rows of x may be strided (its last dimension is dense)."""
+    torch = _mx_torch()
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    code = _mx[2].get(x.dtype)
+    if code is None:
+        raise TypeError(f"x must be float32, bfloat16 or float16, got {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D, got shape {tuple(x.shape)}")
+    if block_rows not in (1, FP8_BLOCK):
+        raise ValueError(f"block_rows must be 1 or {FP8_BLOCK}, got {block_rows}")
+    if not x.is_cuda:
+        raise ValueError(f"x must be on a GPU device, got {x.device}")
+    rows, K = x.shape
+    ldx, step = x.stride()
+    if (K > 1 and step != 1) or (rows > 1 and ldx < K):
+        raise ValueError(f"x must be dense along its last dimension, its rows apart: strides {x.stride()}")
+    U, device = -(-K // FP8_BLOCK), x.device
+    if codes is None:
+        codes = torch.empty((rows, FP8_BLOCK * U), dtype=torch.float8_e4m3fn, device=device)
+    else:
+        _check_given(codes, "codes", _f8_types(), (rows, FP8_BLOCK * U), device)
+    shape = (-(-rows // block_rows), U)
+    if scales is None:
+        scales = torch.empty(shape, dtype=torch.float32, device=device)
+    else:
+        _check_given(scales, "scales", (torch.float32,), shape, device)
+    _mx_launch(_mx[1].lpgemm_fp8_block_quantize, device.index, stream, x.data_ptr(), code, ldx, block_rows, int(bool(power_of_two)),
+               codes.data_ptr(), scales.data_ptr(), rows, K)
+    return codes, scales
+
+
+def _check_given(t, name: str, dtypes, shape, device):
+    _check_on(t, name, dtypes, len(shape), device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def lpgemm_fp8_block_dequantize(codes, scales, K, *, dtype=None, out=None, stream=None):
+    """The values [rows, K] that codes and their scales (per row or per 128 rows)
+    stand for, as bfloat16 (default), float16 or float32."""
+    _mx_torch()
+    units, block_rows = _check_f8(codes, scales, "codes", 2)
+    if K < 0 or -(-K // FP8_BLOCK) != units:
+        raise ValueError(f"K={K} does not fit {units} blocks of {FP8_BLOCK} values")
+    device, rows = codes.device, codes.shape[0]
+    out, code = _mx_out(out, dtype, rows, K, device)
+    _mx_launch(_mx[1].lpgemm_fp8_block_dequantize, device.index, stream, codes.data_ptr(), scales.data_ptr(), block_rows, out.data_ptr(), code, rows, K)
+    return out
+
+
+def lpgemm_fp8_block(A, SFA, B, SFB, *, dtype=None, out=None, stream=None):
+    """D[M,N] = sum over blocks of 128 k of SFA[m,j] SFB[n,j] (A_j . B_j^T): codes
+    float8_e4m3fn or uint8 [M, 128 U] and [N, 128 U], scales float32 [M, U] and
+    [N, U] or [ceil(N / 128), U]; D as bfloat16 (default), float16 or float32 (at
+    about half the speed: sums good to binary32)."""
+    _mx_torch()
+    units, block_rows = _check_f8(A, SFA, "A", 2)
+    M = A.shape[0]
+    if block_rows != 1:
+        raise ValueError(f"A must have a scale for every row and block: shape ({M}, {units}), got {tuple(SFA.shape)}")
+    device = A.device
+    units_b, block_rows = _check_f8(B, SFB, "B", 2, device)
+    if units_b != units:
+        raise ValueError(f"K mismatch: A has {A.shape[1]} codes per row, B {B.shape[1]}")
+    N = B.shape[0]
+    D, code = _mx_out(out, dtype, M, N, device)
+    _mx_launch(_mx[1].lpgemm_fp8_block, device.index, stream, A.data_ptr(), SFA.data_ptr(), B.data_ptr(), SFB.data_ptr(), block_rows, D.data_ptr(),
+               code, M, N, FP8_BLOCK * units)
+    return D
+
+
+def lpgemm_fp8_block_grouped(A, SFA, B, SFB, offsets, *, rows=None, dtype=None, out=None, stream=None):
+    """lpgemm_fp8_block of each group of rows with its own matrix: row i of the
+    result, offsets[e] <= i < offsets[e + 1], is row rows[i] of A times B[e]^T (rows
+    None: row i; an index outside A's rows stands for zeros).  A codes [T, 128 U], B
+    codes [E, N, 128 U] with scales [E, N, U] or [E, ceil(N / 128), U]; offsets int32
+    [E + 1] and rows int32 on the device, as lpgemm_route gives them.  Rows that no
+    group holds are not written: without `out` they are whatever the new tensor's
+    memory held."""
+    _mx_torch()
+    units, block_rows = _check_f8(A, SFA, "A", 2)
+    T = R = A.shape[0]
+    if block_rows != 1:
+        raise ValueError(f"A must have a scale for every row and block: shape ({T}, {units}), got {tuple(SFA.shape)}")
+    device = A.device
+    units_b, block_rows = _check_f8(B, SFB, "B", 3, device)
+    if units_b != units:
+        raise ValueError(f"K mismatch: A has {A.shape[1]} codes per row, B {B.shape[2]}")
+    E, N = B.shape[0], B.shape[1]
+    int32 = (_mx[0].int32,)
+    _check_given(offsets, "offsets", int32, (E + 1,), device)
+    index = None
+    if rows is not None:
+        _check_on(rows, "rows", int32, 1, device)
+        R, index = rows.shape[0], rows.data_ptr()
+    D, code = _mx_out(out, dtype, R, N, device)
+    _mx_launch(_mx[1].lpgemm_fp8_block_grouped, device.index, stream, A.data_ptr(), SFA.data_ptr(), T, index, B.data_ptr(), SFB.data_ptr(), block_rows,
+               E, offsets.data_ptr(), D.data_ptr(), code, R, N, FP8_BLOCK * units)
+    return D
+
+
+def lpgemm_fp8_block_plan(R: int, N: int, K: int, E: int = 0, cu_count: int = 0) -> dict:
+    """Kernel and launch shape of an fp8_block product of R rows (E groups: of a
+    grouped one with R rows of D), host only."""
+    info = PlanInfo()
+    _raise(lib().lpgemm_fp8_block_plan(R, N, K, E, cu_count, ctypes.byref(info)), "lpgemm_fp8_block_plan")
+    return info.as_dict()
+
+
+# ---- experts: routing and the sum of a token's -----------------------------------
+def _route_options(top, score, groups, top_groups, group_top, renormalise, scale):
+    if score not in ROUTE_SCORES:
+        raise ValueError(f"score must be one of {list(ROUTE_SCORES)}, got {score!r}")
+    return RouteOptions(ROUTE_SCORES[score], top, groups, groups if top_groups is None else top_groups, group_top, int(bool(renormalise)), scale)
+
+
+def _route_logits(logits):
+    """(type code, row stride) of [T, E] logits; their rows may be strided."""
+    torch = _mx_torch()
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    code = _mx[2].get(logits.dtype)
+    if code is None:
+        raise TypeError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be 2-D, got shape {tuple(logits.shape)}")
+    if not logits.is_cuda:
+        raise ValueError(f"logits must be on a GPU device, got {logits.device}")
+    (T, E), (ld, step) = logits.shape, logits.stride()
+    if (E > 1 and step != 1) or (T > 1 and ld < E):
+        raise ValueError(f"logits must be dense along their last dimension, their rows apart: strides {logits.stride()}")
+    return code, ld
+
+
+def lpgemm_route_workspace_size(T: int, E: int) -> int:
+    """Bytes of workspace an lpgemm_route call with these sizes needs (host only)."""
+    n = ctypes.c_size_t(0)
+    _raise(lib().lpgemm_route_workspace_size(T, E, ctypes.byref(n)), "lpgemm_route_workspace_size")
+    return int(n.value)
+
+
+def lpgemm_route(logits, top, *, score="softmax", bias=None, groups=1, top_groups=None, group_top=2, renormalise=True, scale=1.0,
+                 workspace="auto", stream=None):
+    """Routing of logits [T, E] (float32, bfloat16 or float16; -inf closes an expert)
+    to each token's `top` experts: Routing(experts int32 [T, top], weights float32 [T,
+    top], rows int32 [T * top], offsets int32 [E + 1], places int32 [T, top]).
+
+    Scores are the softmax of a row or sigmoids; `bias` float32 [E] is added for the
+    choice alone.  With `groups` of neighbouring experts, each scored by the sum of
+    its `group_top` (1 or 2) best choice scores, the experts of the `top_groups`
+    best stay.  Ties go to the lowest index.  A token's weights are its experts'
+    scores, divided by their sum (renormalise), times `scale`.  `rows` and `offsets`
+    are what the grouped products take, `places` what lpgemm_combine does; where a
+    token finds no `top` open experts, the others are -1 with weight 0.  The work-
+    space is allocated ("auto") or a uint8 device tensor."""
+    torch = _mx_torch()
+    code, ld = _route_logits(logits)
+    T, E = logits.shape
+    device = logits.device
+    if bias is not None:
+        _check_given(bias, "bias", (torch.float32,), (E,), device)
+    options = _route_options(top, score, groups, top_groups, group_top, renormalise, scale)
+    if not 1 <= top <= ROUTE_MAX_TOP:
+        raise ValueError(f"top must be 1 .. {ROUTE_MAX_TOP}, got {top}")
+    need = lpgemm_route_workspace_size(T, E)
+    if isinstance(workspace, str) and workspace == "auto":
+        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        if need and stream is not None:  # freed here, in use there
+            workspace.record_stream(stream)
+    elif workspace is not None:
+        _check_on(workspace, "workspace", (torch.uint8,), 1, device)
+    ints = torch.empty(3 * T * top + E + 1, dtype=torch.int32, device=device)
+    experts, places, rows = ints[:T * top].view(T, top), ints[T * top:2 * T * top].view(T, top), ints[2 * T * top:3 * T * top]
+    offsets = ints[3 * T * top:]
+    weights = torch.empty((T, top), dtype=torch.float32, device=device)
+    _mx_launch(_mx[1].lpgemm_route, device.index, stream, logits.data_ptr(), code, ld, None if bias is None else bias.data_ptr(), ctypes.byref(options),
+               experts.data_ptr(), weights.data_ptr(), rows.data_ptr(), offsets.data_ptr(), places.data_ptr(), T, E,
+               None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
+    return Routing(experts, weights, rows, offsets, places)
+
+
+def lpgemm_route_backward(dweights, logits, experts, *, score="softmax", renormalise=True, scale=1.0, out=None, stream=None):
+    """The gradient of the logits [T, E], of their type, from that of lpgemm_route's
+    weights (dweights float32 [T, top]); experts as it gave them, score, renormalise
+    and scale as it took them.  The choice itself has no gradient."""
+    torch = _mx_torch()
+    code, ld = _route_logits(logits)
+    T, E = logits.shape
+    device = logits.device
+    _check_on(experts, "experts", (torch.int32,), 2, device)
+    top = experts.shape[1]
+    if experts.shape[0] != T:
+        raise ValueError(f"experts must have {T} rows, got {experts.shape[0]}")
+    _check_given(dweights, "dweights", (torch.float32,), (T, top), device)
+    options = _route_options(top, score, 1, 1, 1, renormalise, scale)
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=device)
+    else:
+        _check_given(out, "out", (logits.dtype,), (T, E), device)
+    _mx_launch(_mx[1].lpgemm_route_backward, device.index, stream, dweights.data_ptr(), logits.data_ptr(), code, ld, experts.data_ptr(),
+               ctypes.byref(options), out.data_ptr(), T, E)
+    return out
+
+
+def _combine_operands(y, places, weights):
+    torch = _mx_torch()
+    _check_on(y, "y", tuple(_mx[2]), 2)
+    device = y.device
+    _check_on(places, "places", (torch.int32,), 2, device)
+    if weights is not None:
+        _check_given(weights, "weights", (torch.float32,), places.shape, device)
+    return device, *places.shape, *y.shape
+
+
+def lpgemm_combine(y, places, weights=None, *, residual=None, dtype=None, out=None, stream=None):
+    """out[t] = residual[t] + sum_k weights[t, k] y[places[t, k]]: the rows of y [R, N]
+    (float32, bfloat16 or float16) that belong to a token, added in float32 in order;
+    places int32 [T, top] (outside y's rows: nothing is added), weights float32 [T,
+    top] (None: ones), residual [T, N] of the result's type.  The result's type is
+    y's unless `dtype` or `out` says otherwise."""
+    device, T, top, R, N = _combine_operands(y, places, weights)
+    if dtype is None and out is None:
+        dtype = y.dtype
+    out, code = _mx_out(out, dtype, T, N, device)
+    if residual is not None:
+        _check_given(residual, "residual", (out.dtype,), (T, N), device)
+    _mx_launch(_mx[1].lpgemm_combine, device.index, stream, y.data_ptr(), _mx[2][y.dtype], R, places.data_ptr(),
+               None if weights is None else weights.data_ptr(), None if residual is None else residual.data_ptr(), out.data_ptr(), code, T, top, N)
+    return out
+
+
+def lpgemm_combine_backward(dout, y, places, weights=None, *, dy=None, stream=None):
+    """lpgemm_combine's gradients (dy [R, N] of y's type, dweights float32 [T, top])
+    from dout [T, N]; the residual's is dout.  Rows of dy that are in no place are not
+    written (without `dy` they are whatever the new tensor's memory held); no row may
+    be in two."""
+    device, T, top, R, N = _combine_operands(y, places, weights)
+    torch = _mx[0]
+    _check_given(dout, "dout", tuple(_mx[2]), (T, N), device)
+    if dy is None:
+        dy = torch.empty_like(y)
+    else:
+        _check_given(dy, "dy", (y.dtype,), (R, N), device)
+    dweights = torch.empty((T, top), dtype=torch.float32, device=device)
+    _mx_launch(_mx[1].lpgemm_combine_backward, device.index, stream, dout.data_ptr(), _mx[2][dout.dtype], y.data_ptr(), _mx[2][y.dtype], R,
+               places.data_ptr(), None if weights is None else weights.data_ptr(), dy.data_ptr(), dweights.data_ptr(), T, top, N)
+    return dy, dweights

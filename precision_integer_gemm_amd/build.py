@@ -2,9 +2,10 @@
 
     python -m precision_integer_gemm_amd.build
 
-compiles csrc/lpgemm_api.hip (which includes every integer and fp8 kernel) and
-csrc/mxfp4_api.hip (the microscaled 4-bit kernels) with hipcc into
-precision_integer_gemm_amd/_lpgemm.so, next to this file, and the measurement
+compiles csrc/lpgemm_api.hip (which includes every integer and unscaled fp8
+kernel), csrc/mxfp4_api.hip (the microscaled 4-bit kernels),
+csrc/fp8_block_api.hip (e4m3 with block scales) and csrc/routing_api.hip
+(experts' routing) with hipcc into precision_integer_gemm_amd/_lpgemm.so, next to this file, and the measurement
 probe csrc/ceiling_probe.hip into _ceiling.so (loaded only by bench.py).  These
 need hipcc alone.  Where PyTorch for ROCm, Python's headers and g++ are there,
 csrc/tensor_calls.cpp becomes the Python module _tensor_calls.so, the short way
@@ -22,6 +23,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "lpgemm_api.hip")
 MX_SRC = os.path.join(PKG, "csrc", "mxfp4_api.hip")
+F8_SRC = os.path.join(PKG, "csrc", "fp8_block_api.hip")
+ROUTE_SRC = os.path.join(PKG, "csrc", "routing_api.hip")
 LIB = os.path.join(PKG, "_lpgemm.so")
 CALLS_SRC = os.path.join(PKG, "csrc", "tensor_calls.cpp")
 CALLS_LIB = os.path.join(PKG, "_tensor_calls.so")
@@ -95,8 +98,8 @@ def run(cmd: list[str], what: str, verbose: bool) -> None:
 
 
 def build(verbose: bool = False) -> str:
-    objects = [LIB + "." + os.path.basename(src) + ".o" for src in (SRC, MX_SRC)]
-    jobs = [(command(o, src, "-c"), os.path.basename(src)) for o, src in zip(objects, (SRC, MX_SRC))]
+    objects = [LIB + "." + os.path.basename(src) + ".o" for src in (SRC, F8_SRC)]
+    jobs = [(command(o, src, "-c"), os.path.basename(src)) for o, src in zip(objects, (SRC, F8_SRC))]
     jobs.append((command(PROBE_LIB + ".tmp", PROBE_SRC, "-shared"), os.path.basename(PROBE_SRC)))
     missing, calls_obj = calls_missing(), CALLS_LIB + ".o"
     with ThreadPoolExecutor(len(jobs) + 1) as pool:
@@ -105,7 +108,9 @@ def build(verbose: bool = False) -> str:
             calls = pool.submit(run, calls_compile, os.path.basename(CALLS_SRC), verbose)
         for done in [pool.submit(run, cmd, what, verbose) for cmd, what in jobs]:
             done.result()
-    run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", LIB + ".tmp", *objects], "the library", verbose)
+    # the remaining sources are compiled by the command that links; the objects come
+    # first, since hipcc takes what follows a source for sources too
+    run([*command(LIB + ".tmp", "", "-shared")[:-1], *objects, MX_SRC, ROUTE_SRC], "the library", verbose)
     os.replace(PROBE_LIB + ".tmp", PROBE_LIB)
     os.replace(LIB + ".tmp", LIB)
     for o in objects:

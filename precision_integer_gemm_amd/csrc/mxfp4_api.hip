@@ -1,35 +1,12 @@
 // mxfp4_api.hip -- the microscaled 4-bit entry points of the C-ABI: argument
 // checks, kernel selection and launches (contract in include/lpgemm.h).
-#include "lpgemm.h"
-
-#include <algorithm>
-#include <mutex>
-
+#include "api_common.hpp"
 #include "gemm_mxfp4.hpp"
-#include "host_common.hpp"
 #include "mxfp4_quantize.hpp"
 
 using namespace lpgemm;
 
 namespace {
-
-int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b != 0); }
-bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-lpgemm_status launched() { return hipGetLastError() == hipSuccess ? LPGEMM_OK : LPGEMM_ERR_HIP; }
-
-// lpgemm_out_dtype -> OutFormat; -1 for anything but F32, BF16 and F16.
-int format_of(lpgemm_out_dtype d)
-{
-    switch (d) {
-    case LPGEMM_OUT_F32: return OUT_F32;
-    case LPGEMM_OUT_BF16: return OUT_BF16;
-    case LPGEMM_OUT_F16: return OUT_F16;
-    default: return -1;
-    }
-}
-
-uintptr_t element_bytes(int format) { return format == OUT_F32 ? 4u : 2u; }
 
 // rows x K values to or from codes and scales.
 lpgemm_status check_values(const void *x, const void *codes, const void *scales, int format, int64_t rows, int64_t K)
@@ -53,24 +30,6 @@ constexpr int64_t kManyItems = 4 * 256 * 4 * 256;
 // To codes alone, kept / passed by: 16384 x 8192 bf16 63.4 / 59.2, fp32 114 / 113;
 // 8192 x 8192 fp32 56.8 / 56.9, 8192 x 8191 (rows at any address) 57.4 / 61.1.
 constexpr int64_t kPastCaches = 192 << 20;
-
-// A launch has fewer than 2^32 threads, of 256 to a workgroup: launch(first,
-// count, blocks) for the rows in ranges that one holds (2^30 - 64 rows of up to
-// 128 values).
-template <typename Launch>
-lpgemm_status launch_rows(int64_t rows, int64_t items, int64_t block_items, Launch launch)
-{
-    constexpr int64_t kMostBlocks = (1 << 24) - 1;
-    if (rows * items > INT32_MAX * block_items) return LPGEMM_ERR_UNSUPPORTED;
-    const int64_t most = kMostBlocks * block_items / items;
-    for (int64_t first = 0; first < rows; first += most) {
-        const int64_t count = std::min(most, rows - first);
-        launch(first, count, dim3((unsigned)ceil_div(count * items, block_items)));
-        const lpgemm_status st = launched();
-        if (st != LPGEMM_OK) return st;
-    }
-    return LPGEMM_OK;
-}
 
 template <int IN>
 lpgemm_status launch_quantize(const void *x, int64_t ldx, uint8_t *codes, uint8_t *scales, int64_t rows, int64_t K, hipStream_t stream)
@@ -102,21 +61,6 @@ lpgemm_status launch_dequantize(const uint8_t *codes, const uint8_t *scales, voi
                            scales + first * (items / 4), static_cast<uint8_t *>(y) + first * K * (int64_t)element_bytes(OUT), count, (int32_t)K,
                            (uint32_t)items);
     });
-}
-
-constexpr int kMaxDevices = 64;
-constexpr int kXcds = 8;  // MI355X: 8 XCDs, workgroup ids dealt round robin over them
-
-// Dynamic LDS above 64 KB has to be asked for, once per kernel and device.
-template <typename Kernel>
-lpgemm_status allow_lds(Kernel kernel, int bytes, std::once_flag *once, hipError_t *err)
-{
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return LPGEMM_ERR_HIP;
-    std::call_once(once[dev], [&] {
-        err[dev] = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    });
-    return err[dev] == hipSuccess ? LPGEMM_OK : LPGEMM_ERR_HIP;
 }
 
 template <int HM, int FN, int STAGES, int KG, int OUT>
