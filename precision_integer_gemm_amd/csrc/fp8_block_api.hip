@@ -83,6 +83,18 @@ lpgemm_status launch_tiled(const F8Args &g, int64_t blocks, hipStream_t stream)
     return launched();
 }
 
+template <int OUT>
+lpgemm_status launch_large(const F8Args &g, int64_t blocks, hipStream_t stream)
+{
+    static std::once_flag once[kMaxDevices];
+    static hipError_t err[kMaxDevices];
+    const auto kernel = &gemm_fp8_block_large_kernel<OUT>;
+    const lpgemm_status st = allow_lds(kernel, F8Large::lds(LPGEMM_FP8_BLOCK_MAX_GROUPS), once, err);
+    if (st != LPGEMM_OK) return st;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(512), F8Large::lds(g.E), stream, g, (int)ceil_div(g.N, 256), kXcds);
+    return launched();
+}
+
 // ---- the narrow kernel --------------------------------------------------------
 // Sizes it takes: rows of a product, stages of a wave's registers of A (beyond them A
 // comes through the ring, as it does for groups), 32-bit offsets.
@@ -155,22 +167,27 @@ lpgemm_status launch_narrow_any(const F8Args &g, const NarrowPlan &p, hipStream_
 struct Shape {
     int high, wide, lds;
 };
-enum { kShape64, kShape64Split, kShape128, kShape128Deep, kShapeCount };
+enum { kShape64, kShape64Split, kShape128, kShape128Deep, kShape256, kShapeCount };
 Shape shape_of(int shape, int groups)
 {
     switch (shape) {
     case kShape64: return {64, 64, F8Tile<1, 1, 4>::lds(groups, 1)};
     case kShape64Split: return {64, 64, F8Tile<1, 1, 4>::lds(groups, 2)};
     case kShape128: return {128, 128, F8Tile<2, 2, 2>::lds(groups, 1)};
-    default: return {128, 128, F8Tile<2, 2, 4>::lds(groups, 1)};
+    case kShape128Deep: return {128, 128, F8Tile<2, 2, 4>::lds(groups, 1)};
+    default: return {256, 256, F8Large::lds(groups)};
     }
 }
 constexpr int kSplitUnits = 16;  // two windows of scales for each half
+
+// The large kernel has scales of 128 rows of B, and whole windows of them.
+bool large_serves(const F8Args &g) { return g.sb_shift != 0 && g.U >= F8Large::kMinUnits; }
 
 int choose_shape(const F8Args &g, int64_t cu)
 {
     const int64_t groups = g.offsets ? std::min(g.E, g.R) : 1, rows = ceil_div(g.R, groups);
     const int64_t large = groups * ceil_div(rows, 128) * ceil_div(g.N, 128), small = groups * ceil_div(rows, 64) * ceil_div(g.N, 64);
+    if (large_serves(g) && rows > 128 && groups * ceil_div(rows, 256) * ceil_div(g.N, 256) >= 3 * cu / 4) return kShape256;
     if (rows > 64 && large >= cu / 2) return large > cu ? kShape128 : kShape128Deep;
     return small <= cu && g.U >= kSplitUnits ? kShape64Split : kShape64;
 }
@@ -195,7 +212,7 @@ lpgemm_status plan_shape(const F8Args &g, int shape, int64_t cu, F8Plan *p)
     // 32-bit tile counts; at most one ragged row tile a group more than the rows fill
     if (ceil_div(g.R, s.high) + g.E > INT32_MAX / tiles_n) return LPGEMM_ERR_UNSUPPORTED;
     const int64_t most = (ceil_div(g.R, s.high) + (g.offsets ? std::min(g.E, g.R) : 0)) * tiles_n;
-    *p = F8Plan{shape, {}, std::min(most, (s.lds > 80 * 1024 ? 1 : 2) * cu), shape == kShape64Split ? 512 : 256};
+    *p = F8Plan{shape, {}, std::min(most, (s.lds > 80 * 1024 ? 1 : 2) * cu), shape == kShape64Split || shape == kShape256 ? 512 : 256};
     return LPGEMM_OK;
 }
 
@@ -213,6 +230,8 @@ lpgemm_status plan_product(const F8Args &g, int64_t cu, int forced, F8Plan *p)
         return plan_shape(g, choose_shape(g, cu), cu, p);
     case LPGEMM_KERNEL_TILED_64: return plan_shape(g, g.R * (int64_t)g.N > 64 * 64 * cu || g.U < kSplitUnits ? kShape64 : kShape64Split, cu, p);
     case LPGEMM_KERNEL_TILED_256:
+        if (large_serves(g)) return plan_shape(g, kShape256, cu, p);
+        [[fallthrough]];
     case LPGEMM_KERNEL_TILED_128: return plan_shape(g, g.R * (int64_t)g.N > 128 * 128 * cu ? kShape128 : kShape128Deep, cu, p);
     case LPGEMM_KERNEL_SKINNY: return narrow_serves(g) ? narrow() : LPGEMM_ERR_UNSUPPORTED;
     default: return LPGEMM_ERR_UNSUPPORTED;
@@ -226,6 +245,9 @@ lpgemm_status launch_shape(const F8Args &g, const F8Plan &p, hipStream_t stream)
     case kShape64: return launch_tiled<1, 1, 4, 1, ROWS, OUT>(g, p.blocks, stream);
     case kShape64Split: return launch_tiled<1, 1, 4, 2, ROWS, OUT>(g, p.blocks, stream);
     case kShape128: return launch_tiled<2, 2, 2, 1, ROWS, OUT>(g, p.blocks, stream);
+    case kShape256:
+        if constexpr (!ROWS) return launch_large<OUT>(g, p.blocks, stream);
+        return LPGEMM_ERR_UNSUPPORTED;
     default: return launch_tiled<2, 2, 4, 1, ROWS, OUT>(g, p.blocks, stream);
     }
 }

@@ -45,7 +45,8 @@ struct F8Frag {
     }
 };
 
-// p + the products of 64 k, 32 x 32.
+// p + the products of 64 k, 32 x 32.  Constant scale operands of 0 select the MFMA
+// without scales, half the scaled one's code.
 template <bool FINE>
 __device__ __forceinline__ f32x16 f8_mfma32(const F8Frag &b, const F8Frag &a, f32x16 p)
 {
@@ -54,7 +55,7 @@ __device__ __forceinline__ f32x16 f8_mfma32(const F8Frag &b, const F8Frag &a, f3
         for (int q = 0; q < 4; ++q) p = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b.part(q), a.part(q), p, 0, 0, 0);
         return p;
     }
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b.all(), a.all(), p, 0, 0, 0, 127, 0, 127);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b.all(), a.all(), p, 0, 0, 0, 0, 0, 0);
 }
 // The products of 128 k, 16 x 16.
 template <bool FINE>
@@ -66,7 +67,7 @@ __device__ __forceinline__ mx_f32x4 f8_mfma16(const F8Frag &b, const F8Frag &a)
         for (int q = 0; q < 4; ++q) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.part(q), a.part(q), p, 0, 0, 0);
         return p;
     }
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.all(), a.all(), p, 0, 0, 0, 127, 0, 127);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.all(), a.all(), p, 0, 0, 0, 0, 0, 0);
 }
 
 // ---- tiled kernel ------------------------------------------------------------
@@ -343,6 +344,247 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void gemm_fp8_block_tile
         }
         lds_barrier();  // every wave's rows have left it
     }
+}
+
+// ---- large tiles -----------------------------------------------------------
+// Tiles of 64 FM x 256, FM = 1 .. 4 by the group's rows, one workgroup of eight waves (2
+// x 4) per compute unit; a wave holds FM x 2 blocks of 32 x 32 (FM = 4: 128 accumulators,
+// which the scaling's fused multiply-adds need in plain registers, two waves a SIMD).
+//
+// A stage is one unit (128 k), two slots.  A wave keeps its two blocks of B for the stage
+// and reads its FM blocks of A one ahead; block FM - 1 of a stage is contracted while the
+// next stage's first blocks are read, behind the stage's one barrier: there the next
+// stage has landed, and this one's slot has been read out by all waves and is filled
+// again.  A block's sum is scaled and added while the next block's MFMAs run.
+struct F8Large {
+    // Codes: 32 KB a slot for B, then 32 KB a slot for A; scales: 4 KB a window for A's rows
+    // and 1 KB for B's; 1 KB that nobody reads.
+    static constexpr int kSlot = 32768, kA = 2 * kSlot, kScales = 4 * kSlot, kScaleSlot = 4096 + 1024;
+    static constexpr int kNowhere = kScales + 2 * kScaleSlot, kTables = kNowhere + 1024;
+    static constexpr int lds(int groups) { return kTables + 4 * (groups + 1 + 8); }
+    static constexpr int kMinUnits = 4;
+};
+
+template <int OUT>
+__global__ __launch_bounds__(512, 1) void gemm_fp8_block_large_kernel(F8Args g, int tiles_n, int xcds)
+{
+    using C = F8Large;
+    constexpr bool FINE = OUT == OUT_F32;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    int32_t *cum = reinterpret_cast<int32_t *>(smem + C::kTables);
+
+    // computed afresh where it is used: kept through the K loop it would not fit the registers
+    auto opaque_lane = [&]() __attribute__((always_inline)) {
+        int l = (int)threadIdx.x & 63;
+        asm volatile("" : "+v"(l));
+        return l;
+    };
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    const int U = g.U;
+    const uint32_t ldc = (uint32_t)U * kF8UnitCodes, lds_ = (uint32_t)U * kF8UnitScales;
+    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(smem);
+
+    MxGroups groups;
+    if (g.offsets != nullptr) groups.init<8>(g, 256, cum);
+    const int total = (g.offsets == nullptr ? (g.R + 255) / 256 : groups.total) * tiles_n;
+
+    // The current tile: group e, rows [m0, m1) of D, columns from n0, height 64 fm.
+    int e = 0, m0 = 0, m1 = 0, n0 = 0, fm = 0;
+    auto find = [&](int v) __attribute__((always_inline)) {
+        mx_find_tile<4, 4>(g, v, total, tiles_n, xcds, groups, e, m0, m1, n0, fm);
+    };
+
+    // This wave's copies of a stage: rows 32 wave .. + 31 of B, 8 fm wave .. of A; of a
+    // window of scales waves 0 .. 3 64 rows of A each, wave 4 B's.
+    i32x4 rsrc_a, rsrc_b, rsrc_s;
+    uint32_t a_off[4], b_off[2], s_off;
+    auto place = [&]() __attribute__((always_inline)) {
+        const int lane = opaque_lane();
+        const int64_t brow = (int64_t)e * g.N + n0;
+        const uint32_t nrows = (uint32_t)min(256, g.N - n0);
+        const int64_t arow = g.rows == nullptr ? m0 : 0;
+        const uint32_t mrows = (uint32_t)(g.rows == nullptr ? m1 - m0 : g.T);
+        rsrc_b = make_rsrc(g.B + brow * ldc, nrows * ldc);
+        rsrc_a = make_rsrc(g.A + arow * ldc, mrows * ldc);
+        const int64_t srow = (int64_t)e * g.sb_rows + (n0 >> 7);
+        rsrc_s = make_rsrc(wave < 4 ? g.SFA + arow * lds_ : g.SFB + srow * lds_, (wave < 4 ? mrows : (nrows + 127) / 128) * lds_);
+        auto row = [&](int r) __attribute__((always_inline)) -> int {  // source row of tile row r of A, or -1
+            if (r >= 64 * fm) return -1;
+            if (g.rows == nullptr) return r;
+            const int at = m0 + r < m1 ? g.rows[m0 + r] : -1;
+            return at < g.T ? at : -1;
+        };
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (c < 2) b_off[c] = (uint32_t)(32 * wave + 8 * c + (lane >> 3)) * ldc + 16u * (uint32_t)((lane & 7) ^ ((4 * c + (lane >> 4)) & 7));
+            // copy c of A brings rows 8 p .. 8 p + 7, p = fm wave + c
+            const int p = fm * wave + c, at = c < fm ? row(8 * p + (lane >> 3)) : -1;
+            a_off[c] = at >= 0 ? (uint32_t)at * ldc + 16u * (uint32_t)((lane & 7) ^ ((4 * p + (lane >> 4)) & 7)) : kOutOfRange;
+        }
+        const int at = wave < 4 ? row(64 * wave + lane) : wave == 4 && lane < 2 ? lane : -1;
+        s_off = at >= 0 ? (uint32_t)at * lds_ : kOutOfRange;
+    };
+    // Copies of stage k; stages past the row read zeros.
+    auto copy_b = [&](int c, int k) __attribute__((always_inline)) {
+        // copies 2 and 3: 16 rows on, the same chunks
+        const uint32_t o = b_off[c & 1] + (c < 2 ? 0u : 16u * ldc);
+        mx_dma16_at(rsrc_b, k < U ? o : kOutOfRange, (uint32_t)k * kF8UnitCodes, lds0 + (uint32_t)((k & 1) * C::kSlot + (4 * wave + c) * 1024));
+    };
+    auto copy_a = [&](int c, int k) __attribute__((always_inline)) {
+        mx_dma16_at(rsrc_a, k < U ? a_off[c] : kOutOfRange, (uint32_t)k * kF8UnitCodes,
+                    lds0 + (uint32_t)(C::kA + (k & 1) * C::kSlot + (fm * wave + c) * 1024));
+    };
+    // The window that stage k begins, if it begins one, by waves 0 .. 4; else zeros to
+    // nowhere: a branch in the K loop would let the compiler move the sums past it.
+    auto copy_scales = [&](int k) __attribute__((always_inline)) {
+        const int q = k >> 2;
+        const bool due = (k & 3) == 0 && wave < 5;
+        mx_dma16_at(rsrc_s, due && k < U ? s_off : kOutOfRange, (uint32_t)f8_scale_window(q, U) * 4u,
+                    lds0 + (uint32_t)(due ? C::kScales + (q & 1) * C::kScaleSlot + wave * 1024 : C::kNowhere));
+    };
+    auto prologue = [&]() __attribute__((always_inline)) {
+        copy_scales(0);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) copy_b(c, k);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (c < fm) copy_a(c, k);
+        }
+    };
+
+    int v = blockIdx.x;
+    if (v >= total) return;
+    find(v);
+    place();
+    prologue();
+
+    auto run_tile = [&](auto height) __attribute__((always_inline)) {
+        constexpr int FM = decltype(height)::value;
+        const int lane = opaque_lane(), r32 = lane & 31, h = lane >> 5;
+        f32x16 acc[2][FM];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j) acc[i][j] = f32x16{};
+
+        F8Frag fb[2][2], fa[2][2];  // [block][step]; A's in turn
+        float s[FM], waiting = 0.f;  // a stage's scales; the waiting sum's
+        f32x16 p[2];
+        // this lane's chunks of a row: 4 step + 2 h + half, permuted
+        const uint32_t at = (uint32_t)(r32 * 128 + 16 * ((2 * h) ^ ((r32 >> 1) & 7)));
+        auto read = [&](F8Frag (&f)[2], int q, const uint8_t *base) __attribute__((always_inline)) {
+            const i32x4 x = load16(base + (at ^ (uint32_t)(64 * (q >> 1) + 16 * (q & 1))));
+            if (q & 1) f[q >> 1].hi = x;
+            else f[q >> 1].lo = x;
+        };
+        auto base_a = [&](int j, int odd) __attribute__((always_inline)) { return smem + C::kA + odd * C::kSlot + (wm * FM + j) * 4096; };
+        auto base_b = [&](int i, int odd) __attribute__((always_inline)) { return smem + odd * C::kSlot + (wn * 2 + i) * 4096; };
+        auto read_scales = [&](float (&to)[FM], int k) __attribute__((always_inline)) {
+            const int q = k >> 2, d = f8_scale_at(k, q, U);
+            const uint8_t *base = smem + C::kScales + (q & 1) * C::kScaleSlot + 4 * d;
+            const float sb = *reinterpret_cast<const float *>(base + 4096 + 16 * (wn >> 1));
+#pragma unroll
+            for (int j = 0; j < FM; ++j) to[j] = *reinterpret_cast<const float *>(base + (32 * (wm * FM + j) + r32) * 16) * sb;
+        };
+
+        wait_vmcnt<4 + FM>();
+        lds_barrier();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            read(fa[0], q, base_a(0, 0));
+            read(fb[0], q, base_b(0, 0));
+            read(fb[1], q, base_b(1, 0));
+        }
+        read_scales(s, 0);
+        p[1] = f32x16{};  // the block before the first: nothing
+
+        // Stage k, its parity ODD; A's block j sits in fa[(ODD * FM + j) & 1].
+        auto stage = [&](auto parity, int k) __attribute__((always_inline)) {
+            constexpr int ODD = decltype(parity)::value;
+#pragma unroll
+            for (int j = 0; j < FM; ++j) {
+                constexpr int kTurn = ODD * FM;
+                F8Frag(&cur)[2] = fa[(kTurn + j) & 1];
+                F8Frag(&nxt)[2] = fa[(kTurn + j + 1) & 1];
+                const bool last = j == FM - 1;
+                if (last) {
+                    wait_vmcnt<0>();
+                    lds_barrier();
+                }
+                const uint8_t *from = last ? base_a(0, 1 - ODD) : base_a(j + 1, ODD);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    // the block before this one: its sum, accumulator and scale
+                    const int pj = i == 1 ? j : j == 0 ? FM - 1 : j - 1, pi = 1 - i;
+                    const float ps = i == 1 || j > 0 ? s[pj] : waiting;
+                    p[i] = f8_mfma32<FINE>(fb[i][0], cur[0], f32x16{});
+                    __builtin_amdgcn_sched_barrier(0);
+                    read(nxt, 2 * i, from);
+                    read(nxt, 2 * i + 1, from);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) acc[pi][pj][r] = __builtin_fmaf(p[pi][r], ps, acc[pi][pj][r]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    p[i] = f8_mfma32<FINE>(fb[i][1], cur[1], p[i]);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int r = 8; r < 16; ++r) acc[pi][pj][r] = __builtin_fmaf(p[pi][r], ps, acc[pi][pj][r]);
+                    if (last) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) read(fb[i], q, base_b(i, 1 - ODD));
+                        if (i == 0) {
+                            copy_scales(k + 2);
+                            copy_b(0, k + 2);
+                            copy_b(1, k + 2);
+                        } else {
+                            waiting = s[FM - 1];
+                            read_scales(s, k + 1);
+                            copy_b(2, k + 2);
+                            copy_b(3, k + 2);
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (last)
+#pragma unroll
+                    for (int c = 0; c < FM; ++c) copy_a(c, k + 2);
+            }
+        };
+        using even = std::integral_constant<int, 0>;
+        using odd = std::integral_constant<int, 1>;
+        int k = 0;
+        for (; k + 1 < U; k += 2) {
+            stage(even{}, k);
+            stage(odd{}, k + 1);
+        }
+        if (k < U) stage(even{}, k);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[1][FM - 1][r] = __builtin_fmaf(p[1][r], waiting, acc[1][FM - 1][r]);
+        wait_vmcnt<0>();  // copies past the last stage
+
+        const int tm0 = m0, tm1 = m1, tn0 = n0;
+        v += (int)gridDim.x;
+        lds_barrier();  // every wave is done with the ring
+        uint8_t *out_stage = smem + wave * mx_stage_bytes<OUT, 2>();
+#pragma unroll
+        for (int f = 0; f < FM; ++f)
+            mx_store_rows<OUT, 2>(g, out_stage, [&](int w) -> const f32x16 & { return acc[w][f]; }, tm0 + (wm * FM + f) * 32, tm1, tn0 + wn * 64);
+        if (v >= total) return;
+        lds_barrier();  // every wave's rows have left
+        find(v);
+        place();
+        prologue();
+    };
+
+    while (v < total) {
+        if (fm == 4) run_tile(std::integral_constant<int, 4>{});
+        else if (fm == 3) run_tile(std::integral_constant<int, 3>{});
+        else if (fm == 2) run_tile(std::integral_constant<int, 2>{});
+        else run_tile(std::integral_constant<int, 1>{});
+    }
+    wait_vmcnt<0>();
 }
 
 // ---- narrow kernel -------------------------------------------------------------
