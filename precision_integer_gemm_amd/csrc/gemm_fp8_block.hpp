@@ -357,9 +357,9 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void gemm_fp8_block_tile
 // stage has landed, and this one's slot has been read out by all waves and is filled
 // again.  A block's sum is scaled and added while the next block's MFMAs run.
 struct F8Large {
-    // Codes: 32 KB a slot for B, then 32 KB a slot for A; scales: 4 KB a window for A's rows
-    // and 1 KB for B's; 1 KB that nobody reads.
-    static constexpr int kSlot = 32768, kA = 2 * kSlot, kScales = 4 * kSlot, kScaleSlot = 4096 + 1024;
+    // Codes: 32 KB a slot for A, then for B (a slot and block fit a read's offset field);
+    // scales: 4 KB a window for A's rows and 1 KB for B's; 1 KB that nobody reads.
+    static constexpr int kSlot = 32768, kB = 2 * kSlot, kScales = 4 * kSlot, kScaleSlot = 4096 + 1024;
     static constexpr int kNowhere = kScales + 2 * kScaleSlot, kTables = kNowhere + 1024;
     static constexpr int lds(int groups) { return kTables + 4 * (groups + 1 + 8); }
     static constexpr int kMinUnits = 4;
@@ -425,22 +425,27 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_block_large_kernel(F8Args g, 
         const int at = wave < 4 ? row(64 * wave + lane) : wave == 4 && lane < 2 ? lane : -1;
         s_off = at >= 0 ? (uint32_t)at * lds_ : kOutOfRange;
     };
-    // Copies of stage k; stages past the row read zeros.
+    // Copies of stage k; stages past the row read zeros from a resource without bytes.
     auto copy_b = [&](int c, int k) __attribute__((always_inline)) {
+        i32x4 rsrc = rsrc_b;
+        rsrc.z = k < U ? rsrc.z : 0;
         // copies 2 and 3: 16 rows on, the same chunks
-        const uint32_t o = b_off[c & 1] + (c < 2 ? 0u : 16u * ldc);
-        mx_dma16_at(rsrc_b, k < U ? o : kOutOfRange, (uint32_t)k * kF8UnitCodes, lds0 + (uint32_t)((k & 1) * C::kSlot + (4 * wave + c) * 1024));
+        mx_dma16_at(rsrc, b_off[c & 1] + (c < 2 ? 0u : 16u * ldc), (uint32_t)k * kF8UnitCodes,
+                    lds0 + (uint32_t)(C::kB + (k & 1) * C::kSlot + (4 * wave + c) * 1024));
     };
     auto copy_a = [&](int c, int k) __attribute__((always_inline)) {
-        mx_dma16_at(rsrc_a, k < U ? a_off[c] : kOutOfRange, (uint32_t)k * kF8UnitCodes,
-                    lds0 + (uint32_t)(C::kA + (k & 1) * C::kSlot + (fm * wave + c) * 1024));
+        i32x4 rsrc = rsrc_a;
+        rsrc.z = k < U ? rsrc.z : 0;
+        mx_dma16_at(rsrc, a_off[c], (uint32_t)k * kF8UnitCodes, lds0 + (uint32_t)((k & 1) * C::kSlot + (fm * wave + c) * 1024));
     };
     // The window that stage k begins, if it begins one, by waves 0 .. 4; else zeros to
     // nowhere: a branch in the K loop would let the compiler move the sums past it.
     auto copy_scales = [&](int k) __attribute__((always_inline)) {
         const int q = k >> 2;
         const bool due = (k & 3) == 0 && wave < 5;
-        mx_dma16_at(rsrc_s, due && k < U ? s_off : kOutOfRange, (uint32_t)f8_scale_window(q, U) * 4u,
+        i32x4 rsrc = rsrc_s;
+        rsrc.z = due && k < U ? rsrc.z : 0;
+        mx_dma16_at(rsrc, s_off, (uint32_t)f8_scale_window(q, U) * 4u,
                     lds0 + (uint32_t)(due ? C::kScales + (q & 1) * C::kScaleSlot + wave * 1024 : C::kNowhere));
     };
     auto prologue = [&]() __attribute__((always_inline)) {
@@ -473,15 +478,24 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_block_large_kernel(F8Args g, 
         F8Frag fb[2][2], fa[2][2];  // [block][step]; A's in turn
         float s[FM], waiting = 0.f;  // a stage's scales; the waiting sum's
         f32x16 p[2];
-        // this lane's chunks of a row: 4 step + 2 h + half, permuted
-        const uint32_t at = (uint32_t)(r32 * 128 + 16 * ((2 * h) ^ ((r32 >> 1) & 7)));
-        auto read = [&](F8Frag (&f)[2], int q, const uint8_t *base) __attribute__((always_inline)) {
-            const i32x4 x = load16(base + (at ^ (uint32_t)(64 * (q >> 1) + 16 * (q & 1))));
+        // this lane's chunks of a row of A: 4 step + 2 h + half, permuted
+        uint32_t at[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            at[q] = (uint32_t)(wm * FM * 4096 + r32 * 128 + 16 * ((4 * (q >> 1) + 2 * h + (q & 1)) ^ ((r32 >> 1) & 7)));
+        auto read = [&](F8Frag (&f)[2], int q, uint32_t from, int slot) __attribute__((always_inline)) {
+            const i32x4 x = load16(smem + from + slot);
             if (q & 1) f[q >> 1].hi = x;
             else f[q >> 1].lo = x;
         };
-        auto base_a = [&](int j, int odd) __attribute__((always_inline)) { return smem + C::kA + odd * C::kSlot + (wm * FM + j) * 4096; };
-        auto base_b = [&](int i, int odd) __attribute__((always_inline)) { return smem + odd * C::kSlot + (wn * 2 + i) * 4096; };
+        auto read_a = [&](F8Frag (&f)[2], int q, int j, int odd) __attribute__((always_inline)) { read(f, q, at[q], odd * C::kSlot + j * 4096); };
+        // B's are as far behind them for every lane
+        auto read_b = [&](int i, int odd) __attribute__((always_inline)) {
+            uint32_t behind = (uint32_t)(C::kB + wn * 8192 - wm * FM * 4096);
+            asm volatile("" : "+s"(behind));  // four more registers through the loop would not fit
+#pragma unroll
+            for (int q = 0; q < 4; ++q) read(fb[i], q, at[q] + behind, odd * C::kSlot + i * 4096);
+        };
         auto read_scales = [&](float (&to)[FM], int k) __attribute__((always_inline)) {
             const int q = k >> 2, d = f8_scale_at(k, q, U);
             const uint8_t *base = smem + C::kScales + (q & 1) * C::kScaleSlot + 4 * d;
@@ -493,11 +507,9 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_block_large_kernel(F8Args g, 
         wait_vmcnt<4 + FM>();
         lds_barrier();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            read(fa[0], q, base_a(0, 0));
-            read(fb[0], q, base_b(0, 0));
-            read(fb[1], q, base_b(1, 0));
-        }
+        for (int q = 0; q < 4; ++q) read_a(fa[0], q, 0, 0);
+        read_b(0, 0);
+        read_b(1, 0);
         read_scales(s, 0);
         p[1] = f32x16{};  // the block before the first: nothing
 
@@ -511,19 +523,21 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_block_large_kernel(F8Args g, 
                 F8Frag(&nxt)[2] = fa[(kTurn + j + 1) & 1];
                 const bool last = j == FM - 1;
                 if (last) {
-                    wait_vmcnt<0>();
+                    // the next stage has landed; the copies of B behind it stay in flight
+                    wait_vmcnt<FM == 1 ? 0 : 4>();
                     lds_barrier();
                 }
-                const uint8_t *from = last ? base_a(0, 1 - ODD) : base_a(j + 1, ODD);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
+                    // every wave has read this stage's B
+                    if (FM == 2 ? j == 0 && i == 1 : j == 1 && FM > 2 && i == 0) lds_barrier();
                     // the block before this one: its sum, accumulator and scale
                     const int pj = i == 1 ? j : j == 0 ? FM - 1 : j - 1, pi = 1 - i;
                     const float ps = i == 1 || j > 0 ? s[pj] : waiting;
                     p[i] = f8_mfma32<FINE>(fb[i][0], cur[0], f32x16{});
                     __builtin_amdgcn_sched_barrier(0);
-                    read(nxt, 2 * i, from);
-                    read(nxt, 2 * i + 1, from);
+                    read_a(nxt, 2 * i, last ? 0 : j + 1, last ? 1 - ODD : ODD);
+                    read_a(nxt, 2 * i + 1, last ? 0 : j + 1, last ? 1 - ODD : ODD);
 #pragma unroll
                     for (int r = 0; r < 8; ++r) acc[pi][pj][r] = __builtin_fmaf(p[pi][r], ps, acc[pi][pj][r]);
                     __builtin_amdgcn_sched_barrier(0);
@@ -531,25 +545,27 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_block_large_kernel(F8Args g, 
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int r = 8; r < 16; ++r) acc[pi][pj][r] = __builtin_fmaf(p[pi][r], ps, acc[pi][pj][r]);
-                    if (last) {
+                    if (FM == 2 ? j == 0 && i == 1 : j == 1 && FM > 2) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) read(fb[i], q, base_b(i, 1 - ODD));
+                        for (int c = 0; c < 4; ++c)
+                            if (FM == 2 || c / 2 == i) copy_b(c, k + 2);
+                    }
+                    if (last) {
+                        read_b(i, 1 - ODD);
                         if (i == 0) {
-                            copy_scales(k + 2);
-                            copy_b(0, k + 2);
-                            copy_b(1, k + 2);
-                        } else {
                             waiting = s[FM - 1];
+                            copy_scales(k + 2);
+                        } else {
                             read_scales(s, k + 1);
-                            copy_b(2, k + 2);
-                            copy_b(3, k + 2);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if (c < FM && c / 2 == i) copy_a(c, k + 2);
+                            if (FM == 1 && c / 2 == i) copy_b(c, k + 2);
                         }
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                if (last)
-#pragma unroll
-                    for (int c = 0; c < FM; ++c) copy_a(c, k + 2);
             }
         };
         using even = std::integral_constant<int, 0>;
