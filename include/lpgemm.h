@@ -739,7 +739,7 @@ lpgemm_status lpgemm_plan(lpgemm_variant variant, const void *A, const void *B, 
  */
 lpgemm_status lpgemm_mxfp4_plan(int64_t R, int64_t N, int64_t K, int64_t E, int32_t cu_count, lpgemm_plan_info *info);
 
-/* The same for an fp8_block product (b_block_rows 128 or 1). */
+/* The same for an fp8_block product with b_block_rows 128 and a 16-bit result. */
 lpgemm_status lpgemm_fp8_block_plan(int64_t R, int64_t N, int64_t K, int64_t E, int32_t cu_count, lpgemm_plan_info *info);
 
 /*

@@ -180,14 +180,14 @@ Shape shape_of(int shape, int groups)
 }
 constexpr int kSplitUnits = 16;  // two windows of scales for each half
 
-// The large kernel has scales of 128 rows of B, and whole windows of them.
-bool large_serves(const F8Args &g) { return g.sb_shift != 0 && g.U >= F8Large::kMinUnits; }
+// The large kernel has scales of 128 rows of B, whole windows of them, and 16-bit results.
+bool large_serves(const F8Args &g, int format) { return format != OUT_F32 && g.sb_shift != 0 && g.U >= F8Large::kMinUnits; }
 
-int choose_shape(const F8Args &g, int64_t cu)
+int choose_shape(const F8Args &g, int format, int64_t cu)
 {
     const int64_t groups = g.offsets ? std::min(g.E, g.R) : 1, rows = ceil_div(g.R, groups);
     const int64_t large = groups * ceil_div(rows, 128) * ceil_div(g.N, 128), small = groups * ceil_div(rows, 64) * ceil_div(g.N, 64);
-    if (large_serves(g) && rows > 128 && groups * ceil_div(rows, 256) * ceil_div(g.N, 256) >= 3 * cu / 4) return kShape256;
+    if (large_serves(g, format) && rows > 128 && groups * ceil_div(rows, 256) * ceil_div(g.N, 256) >= 3 * cu / 4) return kShape256;
     if (rows > 64 && large >= cu / 2) return large > cu ? kShape128 : kShape128Deep;
     return small <= cu && g.U >= kSplitUnits ? kShape64Split : kShape64;
 }
@@ -216,7 +216,7 @@ lpgemm_status plan_shape(const F8Args &g, int shape, int64_t cu, F8Plan *p)
     return LPGEMM_OK;
 }
 
-lpgemm_status plan_product(const F8Args &g, int64_t cu, int forced, F8Plan *p)
+lpgemm_status plan_product(const F8Args &g, int format, int64_t cu, int forced, F8Plan *p)
 {
     const auto narrow = [&] {
         const NarrowPlan n = plan_narrow(g, cu);
@@ -227,10 +227,10 @@ lpgemm_status plan_product(const F8Args &g, int64_t cu, int forced, F8Plan *p)
     case LPGEMM_KERNEL_AUTO:
     case LPGEMM_KERNEL_TILED:
         if (forced == LPGEMM_KERNEL_AUTO && narrow_serves(g) && narrow_pays(g)) return narrow();
-        return plan_shape(g, choose_shape(g, cu), cu, p);
+        return plan_shape(g, choose_shape(g, format, cu), cu, p);
     case LPGEMM_KERNEL_TILED_64: return plan_shape(g, g.R * (int64_t)g.N > 64 * 64 * cu || g.U < kSplitUnits ? kShape64 : kShape64Split, cu, p);
     case LPGEMM_KERNEL_TILED_256:
-        if (large_serves(g)) return plan_shape(g, kShape256, cu, p);
+        if (large_serves(g, format)) return plan_shape(g, kShape256, cu, p);
         [[fallthrough]];
     case LPGEMM_KERNEL_TILED_128: return plan_shape(g, g.R * (int64_t)g.N > 128 * 128 * cu ? kShape128 : kShape128Deep, cu, p);
     case LPGEMM_KERNEL_SKINNY: return narrow_serves(g) ? narrow() : LPGEMM_ERR_UNSUPPORTED;
@@ -246,7 +246,7 @@ lpgemm_status launch_shape(const F8Args &g, const F8Plan &p, hipStream_t stream)
     case kShape64Split: return launch_tiled<1, 1, 4, 2, ROWS, OUT>(g, p.blocks, stream);
     case kShape128: return launch_tiled<2, 2, 2, 1, ROWS, OUT>(g, p.blocks, stream);
     case kShape256:
-        if constexpr (!ROWS) return launch_large<OUT>(g, p.blocks, stream);
+        if constexpr (!ROWS && OUT != OUT_F32) return launch_large<OUT>(g, p.blocks, stream);
         return LPGEMM_ERR_UNSUPPORTED;
     default: return launch_tiled<2, 2, 4, 1, ROWS, OUT>(g, p.blocks, stream);
     }
@@ -256,7 +256,7 @@ template <int OUT>
 lpgemm_status launch_product(const F8Args &g, hipStream_t stream)
 {
     F8Plan p;
-    const lpgemm_status st = plan_product(g, compute_units(), forced_kernel(), &p);
+    const lpgemm_status st = plan_product(g, OUT, compute_units(), forced_kernel(), &p);
     if (st != LPGEMM_OK) return st;
     if (p.shape == kShapeCount) return launch_narrow_any<OUT>(g, p.narrow, stream);
     return g.sb_shift == 0 ? launch_shape<true, OUT>(g, p, stream) : launch_shape<false, OUT>(g, p, stream);
@@ -371,7 +371,7 @@ lpgemm_status lpgemm_fp8_block_plan(int64_t R, int64_t N, int64_t K, int64_t E, 
     static const int32_t some = 0;  // offsets are there or not, nobody reads them
     const F8Args g = args_of(nullptr, nullptr, R, nullptr, nullptr, nullptr, 7, std::max<int64_t>(E, 1), E > 0 ? &some : nullptr, nullptr, R, N, K);
     F8Plan p;
-    const lpgemm_status st = plan_product(g, cu_count > 0 ? cu_count : 256, forced_kernel(), &p);
+    const lpgemm_status st = plan_product(g, OUT_BF16, cu_count > 0 ? cu_count : 256, forced_kernel(), &p);
     if (st != LPGEMM_OK) return st;
     const bool narrow = p.shape == kShapeCount;
     const Shape s = shape_of(p.shape, 0);

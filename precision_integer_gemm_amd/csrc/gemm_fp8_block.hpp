@@ -95,11 +95,12 @@ struct F8Tile {
     static constexpr int BN = 64 * FN;
     static constexpr int kStages = STAGES;
     static constexpr int NB = 2 * FN;                            // a wave's copies of B per stage
-    static constexpr int copies(int fm) { return NB + 2 * fm; }  // of codes; and one of scales in every fourth stage
+    static constexpr int copies(int fm) { return NB + 2 * fm; }  // of codes; and one of scales, or of nothing
     static constexpr int kCodes = (BN + 64 * HM) * 128;          // of a stage: B's rows, then A's
     static constexpr int kScales = 4096;                         // of four stages: 1 KB a wave, of its 32 FN rows
-    static constexpr int kRing = kStages * kCodes + 2 * kScales;
-    static constexpr int lds(int groups, int kgroups) { return kgroups * kRing + 4 * (groups + 1 + 4 * kgroups); }
+    // 1 KB that nobody reads, and what the lanes hold of up to 64 groups
+    static constexpr int kNowhere = kStages * kCodes + 2 * kScales, kRing = kNowhere + 1024, kGroups = 768;
+    static constexpr int lds(int groups, int kgroups) { return kgroups * kRing + kGroups + 4 * (groups + 1 + 4 * kgroups); }
 };
 
 // KG == 2: eight waves, the second four on the second half of K with a ring of their
@@ -113,7 +114,7 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void gemm_fp8_block_tile
     constexpr int ST = T::kStages;
     constexpr bool FINE = OUT == OUT_F32;
     extern __shared__ __align__(1024) uint8_t smem_all[];
-    int32_t *cum = reinterpret_cast<int32_t *>(smem_all + KG * T::kRing);  // [E + 1]: row tiles before group e
+    int32_t *table = reinterpret_cast<int32_t *>(smem_all + KG * T::kRing), *cum = table + T::kGroups / 4;  // [E + 1]: row tiles before group e
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3;
@@ -129,10 +130,19 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void gemm_fp8_block_tile
     MxGroups groups;
     if (g.offsets != nullptr) groups.init<4 * KG>(g, 64 * HM, cum);
     const int total = (g.offsets == nullptr ? (g.R + 64 * HM - 1) / (64 * HM) : groups.total) * tiles_n;
+    // the lanes' part is put away between tiles: the K loop has few registers for it
+    table[lane] = groups.begin;  // by every wave, the same
+    table[64 + lane] = groups.end;
+    table[128 + lane] = groups.before;
 
     // The current tile: group e, rows [m0, m1) of D, columns from n0, height 64 fm.
     int e = 0, m0 = 0, m1 = 0, n0 = 0, fm = 0;
     auto find = [&](int v) __attribute__((always_inline)) {
+        int at = (int)threadIdx.x & 63;
+        asm volatile("" : "+v"(at));
+        groups.begin = table[at];
+        groups.end = table[64 + at];
+        groups.before = table[128 + at];
         mx_find_tile<HM, FN>(g, v, total, tiles_n, xcds, groups, e, m0, m1, n0, fm);
     };
 
@@ -180,22 +190,21 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void gemm_fp8_block_tile
     auto issue = [&](int j, int f, int local, uint32_t base) __attribute__((always_inline)) {
         const int kt = k0 + local;
         const uint32_t koff = (uint32_t)kt * kF8UnitCodes;
-        if (j < T::NB) {
-            const int p = wave * T::NB + j;
-            mx_dma16_at(rsrc_b, kt < U ? b_off[j] : kOutOfRange, koff, base + (uint32_t)p * 1024u);
-        } else {
-            const int i = j - T::NB, p = wave * 2 * f + i;
-            mx_dma16_at(rsrc_a, kt < U ? a_off[i] : kOutOfRange, koff, base + T::BN * 128 + (uint32_t)p * 1024u);
-        }
+        const int i = j - T::NB, p = j < T::NB ? wave * T::NB + j : wave * 2 * f + i;
+        i32x4 rsrc = j < T::NB ? rsrc_b : rsrc_a;
+        rsrc.z = kt < U ? rsrc.z : 0;
+        mx_dma16_at(rsrc, j < T::NB ? b_off[j < T::NB ? j : 0] : a_off[j < T::NB ? 0 : i], koff, base + (j < T::NB ? 0u : T::BN * 128u) + (uint32_t)p * 1024u);
     };
-    // The scales of stages 4 q .. 4 q + 3.  Rows of fewer than four units have no
-    // window of 16 bytes: theirs are written by hand, and these copies bring zeros to
-    // a place that is not read.
-    auto issue_scales = [&](int q) __attribute__((always_inline)) {
-        const int at = k0 / 4 + q;
-        const bool copied = U >= 4 && 4 * at < U;
-        mx_dma16_at(rsrc_s, copied ? s_off : kOutOfRange, (uint32_t)f8_scale_window(at, U) * 4u,
-                    lds0 + (uint32_t)(ST * T::kCodes + (U >= 4 ? q & 1 : 1) * T::kScales) + (uint32_t)wave * 1024u);
+    // The scales of the window that stage `local` begins, if it begins one; else zeros to
+    // nowhere: a branch in the K loop would let the compiler move the sums past it.  Rows
+    // of fewer than four units have no window of 16 bytes: theirs are written by hand.
+    auto issue_scales = [&](int local) __attribute__((always_inline)) {
+        const int q = local >> 2, at = k0 / 4 + q;
+        const bool due = (local & 3) == 0 && U >= 4;
+        i32x4 rsrc = rsrc_s;
+        rsrc.z = due && 4 * at < U ? rsrc.z : 0;
+        mx_dma16_at(rsrc, s_off, (uint32_t)f8_scale_window(at, U) * 4u,
+                    lds0 + (uint32_t)(due ? ST * T::kCodes + (q & 1) * T::kScales + wave * 1024 : T::kNowhere));
     };
     auto with_height = [&](auto body) __attribute__((always_inline)) {
         if (HM >= 2 && fm == 2) body(std::integral_constant<int, HM >= 2 ? 2 : 1>{});
@@ -225,7 +234,7 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void gemm_fp8_block_tile
         constexpr int C = T::copies(FM);
         constexpr uint32_t kA = T::BN * 128;
         constexpr int kBlocks = FM * FN;
-        wait_vmcnt<(ST - 1) * C>();  // the first stage, and the scales before it
+        wait_vmcnt<(ST - 1) * C>();  // the first stage and the scales before it
         lds_barrier();
 
 #pragma unroll
@@ -276,12 +285,12 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void gemm_fp8_block_tile
         // that refill this one's slot, which all waves have read out before the barrier.
         int slot = 0;
         auto stage = [&](const Stage &cur, Stage &nxt, int kt) __attribute__((always_inline)) {
-            wait_vmcnt<(ST - 2) * C>();  // the next stage, and its scales
+            wait_vmcnt<(ST - 2) * C>();  // the next stage and its scales; fewer are in flight behind them at first
             lds_barrier();
             const uint32_t refill = lds0 + (uint32_t)(slot * T::kCodes);
             slot = slot + 1 == ST ? 0 : slot + 1;
             const uint8_t *next = smem + slot * T::kCodes;
-            if (((kt + ST) & 3) == 0) issue_scales((kt + ST) >> 2);
+            issue_scales(kt + ST);
             read_scales(nxt, kt + 1);
             constexpr int kPer = (kReads + kBlocks - 1) / kBlocks;
 #pragma unroll
@@ -358,9 +367,10 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void gemm_fp8_block_tile
 // again.  A block's sum is scaled and added while the next block's MFMAs run.
 struct F8Large {
     // Codes: 32 KB a slot for A, then for B (a slot and block fit a read's offset field);
-    // scales: 4 KB a window for A's rows and 1 KB for B's; 1 KB that nobody reads.
+    // scales: 4 KB a window for A's rows and 1 KB for B's; 1 KB that nobody reads; what
+    // the lanes hold of up to 64 groups.
     static constexpr int kSlot = 32768, kB = 2 * kSlot, kScales = 4 * kSlot, kScaleSlot = 4096 + 1024;
-    static constexpr int kNowhere = kScales + 2 * kScaleSlot, kTables = kNowhere + 1024;
+    static constexpr int kNowhere = kScales + 2 * kScaleSlot, kGroups = kNowhere + 1024, kTables = kGroups + 768;
     static constexpr int lds(int groups) { return kTables + 4 * (groups + 1 + 8); }
     static constexpr int kMinUnits = 4;
 };
@@ -369,7 +379,7 @@ template <int OUT>
 __global__ __launch_bounds__(512, 1) void gemm_fp8_block_large_kernel(F8Args g, int tiles_n, int xcds)
 {
     using C = F8Large;
-    constexpr bool FINE = OUT == OUT_F32;
+    static_assert(OUT != OUT_F32, "binary32 sums' operands take more registers than are left");
     extern __shared__ __align__(1024) uint8_t smem[];
     int32_t *cum = reinterpret_cast<int32_t *>(smem + C::kTables);
 
@@ -388,10 +398,19 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_block_large_kernel(F8Args g, 
     MxGroups groups;
     if (g.offsets != nullptr) groups.init<8>(g, 256, cum);
     const int total = (g.offsets == nullptr ? (g.R + 255) / 256 : groups.total) * tiles_n;
+    // the lanes' part is put away between tiles: the K loop has no registers for it
+    int32_t *held = reinterpret_cast<int32_t *>(smem + C::kGroups) + (threadIdx.x & 63);
+    held[0] = groups.begin;  // by every wave, the same
+    held[64] = groups.end;
+    held[128] = groups.before;
 
     // The current tile: group e, rows [m0, m1) of D, columns from n0, height 64 fm.
     int e = 0, m0 = 0, m1 = 0, n0 = 0, fm = 0;
     auto find = [&](int v) __attribute__((always_inline)) {
+        const int32_t *held = reinterpret_cast<const int32_t *>(smem + C::kGroups) + opaque_lane();
+        groups.begin = held[0];
+        groups.end = held[64];
+        groups.before = held[128];
         mx_find_tile<4, 4>(g, v, total, tiles_n, xcds, groups, e, m0, m1, n0, fm);
     };
 
@@ -448,23 +467,21 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_block_large_kernel(F8Args g, 
         mx_dma16_at(rsrc, s_off, (uint32_t)f8_scale_window(q, U) * 4u,
                     lds0 + (uint32_t)(due ? C::kScales + (q & 1) * C::kScaleSlot + wave * 1024 : C::kNowhere));
     };
-    auto prologue = [&]() __attribute__((always_inline)) {
-        copy_scales(0);
+    auto begin_stage = [&](int k) __attribute__((always_inline)) {
+        if (k == 0) copy_scales(0);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int c = 0; c < 4; ++c) copy_b(c, k);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) copy_b(c, k);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (c < fm) copy_a(c, k);
-        }
+        for (int c = 0; c < 4; ++c)
+            if (c < fm) copy_a(c, k);
     };
 
     int v = blockIdx.x;
     if (v >= total) return;
     find(v);
     place();
-    prologue();
+    begin_stage(0);
+    begin_stage(1);
 
     auto run_tile = [&](auto height) __attribute__((always_inline)) {
         constexpr int FM = decltype(height)::value;
@@ -534,14 +551,14 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_block_large_kernel(F8Args g, 
                     // the block before this one: its sum, accumulator and scale
                     const int pj = i == 1 ? j : j == 0 ? FM - 1 : j - 1, pi = 1 - i;
                     const float ps = i == 1 || j > 0 ? s[pj] : waiting;
-                    p[i] = f8_mfma32<FINE>(fb[i][0], cur[0], f32x16{});
+                    p[i] = f8_mfma32<false>(fb[i][0], cur[0], f32x16{});
                     __builtin_amdgcn_sched_barrier(0);
                     read_a(nxt, 2 * i, last ? 0 : j + 1, last ? 1 - ODD : ODD);
                     read_a(nxt, 2 * i + 1, last ? 0 : j + 1, last ? 1 - ODD : ODD);
 #pragma unroll
                     for (int r = 0; r < 8; ++r) acc[pi][pj][r] = __builtin_fmaf(p[pi][r], ps, acc[pi][pj][r]);
                     __builtin_amdgcn_sched_barrier(0);
-                    p[i] = f8_mfma32<FINE>(fb[i][1], cur[1], p[i]);
+                    p[i] = f8_mfma32<false>(fb[i][1], cur[1], p[i]);
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int r = 8; r < 16; ++r) acc[pi][pj][r] = __builtin_fmaf(p[pi][r], ps, acc[pi][pj][r]);
@@ -583,15 +600,21 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_block_large_kernel(F8Args g, 
         const int tm0 = m0, tm1 = m1, tn0 = n0;
         v += (int)gridDim.x;
         lds_barrier();  // every wave is done with the ring
-        uint8_t *out_stage = smem + wave * mx_stage_bytes<OUT, 2>();
+        // the next tile's first stage is on its way while the rows leave through the second slot
+        const bool more = v < total;
+        if (more) {
+            find(v);
+            place();
+            begin_stage(0);
+        }
+        static_assert(4 * mx_stage_bytes<OUT, 2>() <= C::kSlot, "half of the second slot holds four waves' rows");
+        uint8_t *out_stage = smem + C::kSlot + wn * mx_stage_bytes<OUT, 2>() + wm * C::kB;
 #pragma unroll
         for (int f = 0; f < FM; ++f)
             mx_store_rows<OUT, 2>(g, out_stage, [&](int w) -> const f32x16 & { return acc[w][f]; }, tm0 + (wm * FM + f) * 32, tm1, tn0 + wn * 64);
-        if (v >= total) return;
+        if (!more) return;
         lds_barrier();  // every wave's rows have left
-        find(v);
-        place();
-        prologue();
+        begin_stage(1);
     };
 
     while (v < total) {
