@@ -522,6 +522,7 @@ _mx = None  # torch, the library, the result types' codes and the native calls, 
 class _LongWay:
     """In the native calls' place where they are not built: every call goes through the checks here."""
     quantize = dequantize = product = grouped = staticmethod(lambda *args: None)
+    block_quantize = block_dequantize = block_product = block_grouped = route = combine = quantize
 
 
 def _mx_torch():
@@ -763,6 +764,10 @@ def lpgemm_fp8_block_quantize(x, *, block_rows=1, power_of_two=False, codes=None
     largest magnitude / 448, or with power_of_two the power of two above that.
     Rows of x may be strided (its last dimension is dense)."""
     torch = _mx_torch()
+    if codes is None and scales is None and stream is None:
+        made = _mx[3].block_quantize(x, block_rows, power_of_two)
+        if made is not None:
+            return made
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     code = _mx[2].get(x.dtype)
@@ -803,6 +808,10 @@ def lpgemm_fp8_block_dequantize(codes, scales, K, *, dtype=None, out=None, strea
     """The values [rows, K] that codes and their scales (per row or per 128 rows)
     stand for, as bfloat16 (default), float16 or float32."""
     _mx_torch()
+    if out is None and stream is None:
+        made = _mx[3].block_dequantize(codes, scales, K, dtype)
+        if made is not None:
+            return made
     units, block_rows = _check_f8(codes, scales, "codes", 2)
     if K < 0 or -(-K // FP8_BLOCK) != units:
         raise ValueError(f"K={K} does not fit {units} blocks of {FP8_BLOCK} values")
@@ -818,6 +827,10 @@ def lpgemm_fp8_block(A, SFA, B, SFB, *, dtype=None, out=None, stream=None):
     [N, U] or [ceil(N / 128), U]; D as bfloat16 (default), float16 or float32 (at
     about half the speed: sums good to binary32)."""
     _mx_torch()
+    if out is None and stream is None:
+        made = _mx[3].block_product(A, SFA, B, SFB, dtype)
+        if made is not None:
+            return made
     units, block_rows = _check_f8(A, SFA, "A", 2)
     M = A.shape[0]
     if block_rows != 1:
@@ -842,6 +855,10 @@ def lpgemm_fp8_block_grouped(A, SFA, B, SFB, offsets, *, rows=None, dtype=None, 
     group holds are not written: without `out` they are whatever the new tensor's
     memory held."""
     _mx_torch()
+    if out is None and stream is None:
+        made = _mx[3].block_grouped(A, SFA, B, SFB, offsets, rows, dtype)
+        if made is not None:
+            return made
     units, block_rows = _check_f8(A, SFA, "A", 2)
     T = R = A.shape[0]
     if block_rows != 1:
@@ -918,6 +935,10 @@ def lpgemm_route(logits, top, *, score="softmax", bias=None, groups=1, top_group
     token finds no `top` open experts, the others are -1 with weight 0.  The work-
     space is allocated ("auto") or a uint8 device tensor."""
     torch = _mx_torch()
+    if stream is None and isinstance(workspace, str) and workspace == "auto":
+        made = _mx[3].route(logits, top, ROUTE_SCORES.get(score), bias, groups, groups if top_groups is None else top_groups, group_top, renormalise, scale)
+        if made is not None:
+            return tuple.__new__(Routing, made)
     code, ld = _route_logits(logits)
     T, E = logits.shape
     device = logits.device
@@ -982,6 +1003,11 @@ def lpgemm_combine(y, places, weights=None, *, residual=None, dtype=None, out=No
     places int32 [T, top] (outside y's rows: nothing is added), weights float32 [T,
     top] (None: ones), residual [T, N] of the result's type.  The result's type is
     y's unless `dtype` or `out` says otherwise."""
+    _mx_torch()
+    if out is None and stream is None:
+        made = _mx[3].combine(y, places, weights, residual, dtype)
+        if made is not None:
+            return made
     device, T, top, R, N = _combine_operands(y, places, weights)
     if dtype is None and out is None:
         dtype = y.dtype

@@ -96,9 +96,12 @@ lpgemm_status launch_large(const F8Args &g, int64_t blocks, hipStream_t stream)
 }
 
 // ---- the narrow kernel --------------------------------------------------------
-// Sizes it takes: rows of a product, stages of a wave's registers of A (beyond them A
-// comes through the ring, as it does for groups), 32-bit offsets.
-constexpr int kNarrowMaxRows = 4096, kNarrowStages = 4;
+// Sizes it takes: rows of a product, stages of a wave's registers of A for up to 16 rows
+// and for more (beyond them A comes through the ring, as it does for groups), 32-bit
+// offsets.  Four stages of 32 rows would not fit the registers.
+constexpr int kNarrowMaxRows = 4096;
+int narrow_stages(int64_t rows) { return rows <= 16 ? 4 : 2; }
+int64_t narrow_units(int64_t rows) { return kF8NarrowUnits * kMxNarrowWaves * narrow_stages(rows); }
 
 bool narrow_serves(const F8Args &g)
 {
@@ -119,14 +122,14 @@ struct NarrowPlan {
 
 NarrowPlan plan_narrow(const F8Args &g, int64_t cu)
 {
-    const bool grouped = g.offsets != nullptr, ring = grouped || g.U > kF8NarrowUnits * kMxNarrowWaves * kNarrowStages;
+    const bool grouped = g.offsets != nullptr, ring = grouped || g.U > narrow_units(g.R);
     const int64_t row_tiles = ceil_div(g.R, g.R <= 16 ? 16 : 32);
     const int64_t strips = ceil_div(g.N, 16) * (grouped ? std::min(g.E, g.R) : ring ? ceil_div(g.R, 16) : 1);
     const int64_t per_tile = ring ? cu : std::max<int64_t>(1, cu / row_tiles);  // workgroups
     NarrowPlan best{kMxNarrowWaves, 1, 0, 0, 0, ring};
     for (int w = kMxNarrowWaves; w > 0; w /= 2) {
         int64_t s = std::max<int64_t>(1, ceil_div(g.U, kF8NarrowUnits * w));
-        if (!ring && s > kNarrowStages) continue;
+        if (!ring && s > narrow_stages(g.R)) continue;
         if (!ring && s == 3) s = 4;  // registers for 1, 2 or 4
         const double t = 1.35 * (double)ceil_div(strips, per_tile * (kMxNarrowWaves / w)) * ((double)s + 1.2);
         if (best.time == 0 || t < best.time) best = {w, (int)s, t, 0, 0, ring};
@@ -158,44 +161,92 @@ lpgemm_status launch_narrow_any(const F8Args &g, const NarrowPlan &p, hipStream_
         return p.stages == 1   ? launch_narrow<1, 1, false, OUT>(g, p, stream)
                : p.stages == 2 ? launch_narrow<1, 2, false, OUT>(g, p, stream)
                                : launch_narrow<1, 4, false, OUT>(g, p, stream);
-    return p.stages == 1   ? launch_narrow<2, 1, false, OUT>(g, p, stream)
-           : p.stages == 2 ? launch_narrow<2, 2, false, OUT>(g, p, stream)
-                           : launch_narrow<2, 4, false, OUT>(g, p, stream);
+    return p.stages == 1 ? launch_narrow<2, 1, false, OUT>(g, p, stream) : launch_narrow<2, 2, false, OUT>(g, p, stream);
 }
 
 // ---- the choice ---------------------------------------------------------------
+// The tiled kernels' shapes and what one of their tiles costs: us for a stage at heights
+// of 64, 128, 192 and 256 rows with every compute unit busy, where tiles are fewer than
+// those, and for a tile.  Fitted on MI355X; where they meet (us, bf16, 64 x 64 / 128 x 128
+// / 256 x 256):
+//     1024 x 1024 x 4096   12.8 / 23.5 / 42.4     2048 x 4096 x 4096   66.5 / 40.6 / 44.7
+//     512 x 4096 x 4096    20.3 / 23.8 / 42.7     2848 x 2880 x 3200   53.9 / 48.5 / 39.0
+//     1024 x 4096 x 4096   35.9 / 25.6 / 43.3     4096 x 4096 x 4096      - / 77.9 / 61.4
+//     200 x 8582 x 6277    36.4 / 34.0 / 64.0     513 x 6086 x 384     10.2 /  8.1 /    -
+// 32 groups of 4096 x 4096, rows shared out by chance:
+//     1024 rows  111 / 121 / 129    4096 rows  223 / 157 / 142    16384 rows  646 / 403 / 296
 struct Shape {
     int high, wide, lds;
+    double stage[4], few, tile;
 };
 enum { kShape64, kShape64Split, kShape128, kShape128Deep, kShape256, kShapeCount };
 Shape shape_of(int shape, int groups)
 {
     switch (shape) {
-    case kShape64: return {64, 64, F8Tile<1, 1, 4>::lds(groups, 1)};
-    case kShape64Split: return {64, 64, F8Tile<1, 1, 4>::lds(groups, 2)};
-    case kShape128: return {128, 128, F8Tile<2, 2, 2>::lds(groups, 1)};
-    case kShape128Deep: return {128, 128, F8Tile<2, 2, 4>::lds(groups, 1)};
-    default: return {256, 256, F8Large::lds(groups)};
+    case kShape64: return {64, 64, F8Tile<1, 1, 4>::lds(groups, 1), {0.26}, 0.34, 1.5};
+    case kShape64Split: return {64, 64, F8Tile<1, 1, 4>::lds(groups, 2), {0.26}, 0.26, 2.5};
+    case kShape128: return {128, 128, F8Tile<2, 2, 2>::lds(groups, 1), {0.45, 0.60}, 0.72, 2.0};
+    case kShape128Deep: return {128, 128, F8Tile<2, 2, 4>::lds(groups, 1), {0.50, 0.72}, 0.72, 2.0};
+    default: return {256, 256, F8Large::lds(groups), {0.85, 1.10, 1.40, 1.72}, 1.40, 4.0};
     }
 }
-constexpr int kSplitUnits = 16;  // two windows of scales for each half
+constexpr int kSplitUnits = 16;       // two windows of scales for each half
+constexpr double kMemory = 4.9e6;     // bytes of matrices a us, whatever the shape
 
-// The large kernel has scales of 128 rows of B, whole windows of them, and 16-bit results.
-bool large_serves(const F8Args &g, int format) { return format != OUT_F32 && g.sb_shift != 0 && g.U >= F8Large::kMinUnits; }
-
-int choose_shape(const F8Args &g, int format, int64_t cu)
+// Which results and scales a shape has: the large kernel's K loop has registers for one
+// scale a tile's columns and 16-bit results alone; a scale for every row of B takes 64 x 64.
+bool serves(const F8Args &g, int format, int shape)
 {
-    const int64_t groups = g.offsets ? std::min(g.E, g.R) : 1, rows = ceil_div(g.R, groups);
-    const int64_t large = groups * ceil_div(rows, 128) * ceil_div(g.N, 128), small = groups * ceil_div(rows, 64) * ceil_div(g.N, 64);
-    if (large_serves(g, format) && rows > 128 && groups * ceil_div(rows, 256) * ceil_div(g.N, 256) >= 3 * cu / 4) return kShape256;
-    if (rows > 64 && large >= cu / 2) return large > cu ? kShape128 : kShape128Deep;
-    return small <= cu && g.U >= kSplitUnits ? kShape64Split : kShape64;
+    if (shape == kShape256) return format != OUT_F32 && g.sb_shift != 0 && g.U >= F8Large::kMinUnits;
+    return shape == kShape64 || (shape == kShape64Split ? g.U >= kSplitUnits : g.sb_shift != 0);
 }
 
-bool narrow_pays(const F8Args &g)
+int64_t tiles_of(const F8Args &g, const Shape &s, int64_t *blocks)
+{
+    const int64_t groups = g.offsets ? std::min(g.E, g.R) : 1, rows = ceil_div(g.R, groups);
+    // groups of different sizes have half a tile more than their average's rows fill
+    const int64_t tiles = g.offsets ? std::max<int64_t>(groups, (2 * (int64_t)g.R + groups * s.high) / (2 * s.high)) : ceil_div(rows, s.high);
+    *blocks = std::min<int64_t>(4, ceil_div(ceil_div(rows, 64), ceil_div(rows, s.high)));
+    return tiles * ceil_div(g.N, s.wide);
+}
+
+// The shape that should take the least time; the smaller of equal ones.
+int choose_shape(const F8Args &g, int format, int64_t cu, double *time)
+{
+    int best = kShape64;
+    *time = 0;
+    for (int i = 0; i < kShapeCount; ++i) {
+        if (!serves(g, format, i)) continue;
+        const Shape s = shape_of(i, 0);
+        int64_t blocks;
+        const int64_t tiles = tiles_of(g, s, &blocks);
+        // one tile to a compute unit: K in two halves, a ring of four stages
+        if ((i == kShape64Split || i == kShape128Deep) && tiles > cu) continue;
+        if (i == kShape128 && tiles <= cu) continue;
+        const double stage = tiles < cu * 3 / 4 ? std::min(s.few, s.stage[blocks - 1] * 1.3) : s.stage[blocks - 1];
+        const double own = (double)ceil_div(tiles, cu) * ((double)g.U * stage + s.tile);
+        const double t = std::max(own, (double)std::min(g.E, g.R) * g.N * g.U * kF8UnitCodes / kMemory);
+        if (*time == 0 || t < *time) {
+            best = i;
+            *time = t;
+        }
+    }
+    return best;
+}
+
+// Whether the narrow kernel takes a call that it can serve: up to 16 rows, up to 32 with
+// A in registers, and few tiles with long K, which its waves split (us, best tiles /
+// narrow):
+//     16 x 28672 x 8192   50.5 / 40.6      32 x 28672 x 8192   50.9 / 74.5
+//     1 x 4096 x 4096     11.1 /  5.6      64 x 4096 x 4096    11.6 / 17.9
+//     32 x 4096 x 4096    11.3 /  9.6      100 x 100 x 16384   30.1 / 15.3
+// Grouped, up to eight rows a group on average (32 groups of 4096 x 4096 by chance):
+//     32 rows  83.4 / 73.1     256 rows  113 / 94     384 rows  117 / 115     512 rows  116 / 133
+bool narrow_pays(const F8Args &g, int64_t cu)
 {
     if (g.offsets != nullptr) return g.R <= 8 * (int64_t)g.E;
-    return g.R <= 32;
+    if (g.R <= 32) return g.R <= 16 || g.U <= narrow_units(g.R);
+    return g.U >= 32 && ceil_div(g.R, 64) * ceil_div(g.N, 64) <= cu / 16;
 }
 
 struct F8Plan {
@@ -225,30 +276,21 @@ lpgemm_status plan_product(const F8Args &g, int format, int64_t cu, int forced, 
     };
     switch (forced) {
     case LPGEMM_KERNEL_AUTO:
-    case LPGEMM_KERNEL_TILED:
-        if (forced == LPGEMM_KERNEL_AUTO && narrow_serves(g) && narrow_pays(g)) return narrow();
-        return plan_shape(g, choose_shape(g, format, cu), cu, p);
-    case LPGEMM_KERNEL_TILED_64: return plan_shape(g, g.R * (int64_t)g.N > 64 * 64 * cu || g.U < kSplitUnits ? kShape64 : kShape64Split, cu, p);
+    case LPGEMM_KERNEL_TILED: {
+        if (forced == LPGEMM_KERNEL_AUTO && narrow_serves(g) && narrow_pays(g, cu)) return narrow();
+        double time;
+        return plan_shape(g, choose_shape(g, format, cu, &time), cu, p);
+    }
     case LPGEMM_KERNEL_TILED_256:
-        if (large_serves(g, format)) return plan_shape(g, kShape256, cu, p);
+        if (serves(g, format, kShape256)) return plan_shape(g, kShape256, cu, p);
         [[fallthrough]];
-    case LPGEMM_KERNEL_TILED_128: return plan_shape(g, g.R * (int64_t)g.N > 128 * 128 * cu ? kShape128 : kShape128Deep, cu, p);
+    case LPGEMM_KERNEL_TILED_128:
+        if (serves(g, format, kShape128)) return plan_shape(g, g.R * (int64_t)g.N > 128 * 128 * cu ? kShape128 : kShape128Deep, cu, p);
+        [[fallthrough]];
+    case LPGEMM_KERNEL_TILED_64:
+        return plan_shape(g, g.R * (int64_t)g.N > 64 * 64 * cu || !serves(g, format, kShape64Split) ? kShape64 : kShape64Split, cu, p);
     case LPGEMM_KERNEL_SKINNY: return narrow_serves(g) ? narrow() : LPGEMM_ERR_UNSUPPORTED;
     default: return LPGEMM_ERR_UNSUPPORTED;
-    }
-}
-
-template <bool ROWS, int OUT>
-lpgemm_status launch_shape(const F8Args &g, const F8Plan &p, hipStream_t stream)
-{
-    switch (p.shape) {
-    case kShape64: return launch_tiled<1, 1, 4, 1, ROWS, OUT>(g, p.blocks, stream);
-    case kShape64Split: return launch_tiled<1, 1, 4, 2, ROWS, OUT>(g, p.blocks, stream);
-    case kShape128: return launch_tiled<2, 2, 2, 1, ROWS, OUT>(g, p.blocks, stream);
-    case kShape256:
-        if constexpr (!ROWS && OUT != OUT_F32) return launch_large<OUT>(g, p.blocks, stream);
-        return LPGEMM_ERR_UNSUPPORTED;
-    default: return launch_tiled<2, 2, 4, 1, ROWS, OUT>(g, p.blocks, stream);
     }
 }
 
@@ -258,8 +300,17 @@ lpgemm_status launch_product(const F8Args &g, hipStream_t stream)
     F8Plan p;
     const lpgemm_status st = plan_product(g, OUT, compute_units(), forced_kernel(), &p);
     if (st != LPGEMM_OK) return st;
-    if (p.shape == kShapeCount) return launch_narrow_any<OUT>(g, p.narrow, stream);
-    return g.sb_shift == 0 ? launch_shape<true, OUT>(g, p, stream) : launch_shape<false, OUT>(g, p, stream);
+    const bool rows = g.sb_shift == 0;
+    switch (p.shape) {
+    case kShape64: return rows ? launch_tiled<1, 1, 4, 1, true, OUT>(g, p.blocks, stream) : launch_tiled<1, 1, 4, 1, false, OUT>(g, p.blocks, stream);
+    case kShape64Split: return rows ? launch_tiled<1, 1, 4, 2, true, OUT>(g, p.blocks, stream) : launch_tiled<1, 1, 4, 2, false, OUT>(g, p.blocks, stream);
+    case kShape128: return launch_tiled<2, 2, 2, 1, false, OUT>(g, p.blocks, stream);
+    case kShape128Deep: return launch_tiled<2, 2, 4, 1, false, OUT>(g, p.blocks, stream);
+    case kShape256:
+        if constexpr (OUT != OUT_F32) return launch_large<OUT>(g, p.blocks, stream);
+        return LPGEMM_ERR_UNSUPPORTED;
+    default: return launch_narrow_any<OUT>(g, p.narrow, stream);
+    }
 }
 
 // Sizes and pointers that both products share; R rows of D.
