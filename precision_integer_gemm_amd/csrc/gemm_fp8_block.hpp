@@ -95,7 +95,7 @@ struct F8Tile {
     static constexpr int BN = 64 * FN;
     static constexpr int kStages = STAGES;
     static constexpr int NB = 2 * FN;                            // a wave's copies of B per stage
-    static constexpr int copies(int fm) { return NB + 2 * fm; }  // of codes; and one of scales, or of nothing
+    static constexpr int copies(int fm) { return NB + 2 * fm; }  // of codes; before them one of scales, or of nothing
     static constexpr int kCodes = (BN + 64 * HM) * 128;          // of a stage: B's rows, then A's
     static constexpr int kScales = 4096;                         // of four stages: 1 KB a wave, of its 32 FN rows
     // 1 KB that nobody reads, and what the lanes hold of up to 64 groups
@@ -220,11 +220,12 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void gemm_fp8_block_tile
         }
         with_height([&](auto height) __attribute__((always_inline)) {
             constexpr int FM = decltype(height)::value;
-            issue_scales(0);
 #pragma unroll
-            for (int st = 0; st < ST; ++st)
+            for (int st = 0; st < ST; ++st) {
+                issue_scales(st);
 #pragma unroll
                 for (int j = 0; j < T::copies(FM); ++j) issue(j, FM, st, lds0 + (uint32_t)(st * T::kCodes));
+            }
         });
     };
 
@@ -234,7 +235,7 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void gemm_fp8_block_tile
         constexpr int C = T::copies(FM);
         constexpr uint32_t kA = T::BN * 128;
         constexpr int kBlocks = FM * FN;
-        wait_vmcnt<(ST - 1) * C>();  // the first stage and the scales before it
+        wait_vmcnt<(ST - 1) * (C + 1)>();  // the first stage and its scales
         lds_barrier();
 
 #pragma unroll
@@ -285,7 +286,7 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void gemm_fp8_block_tile
         // that refill this one's slot, which all waves have read out before the barrier.
         int slot = 0;
         auto stage = [&](const Stage &cur, Stage &nxt, int kt) __attribute__((always_inline)) {
-            wait_vmcnt<(ST - 2) * C>();  // the next stage and its scales; fewer are in flight behind them at first
+            wait_vmcnt<(ST - 2) * (C + 1)>();  // the next stage and its scales
             lds_barrier();
             const uint32_t refill = lds0 + (uint32_t)(slot * T::kCodes);
             slot = slot + 1 == ST ? 0 : slot + 1;

@@ -14,7 +14,7 @@
 // expert's is a population count, whatever order the waves come in.
 #pragma once
 
-#include "gemm_mxfp4.hpp"
+#include "fp8_block_quantize.hpp"
 
 namespace lpgemm {
 
@@ -28,7 +28,7 @@ struct RouteArgs {
     int32_t *rows;       // [T top]
     int32_t *offsets;    // [E + 1]
     int32_t *places;     // [T][top]
-    int32_t *counts;     // [workgroups][E], for several workgroups
+    uint16_t *counts;    // [workgroups][E rounded up to 2], for several workgroups
     int64_t ldl;
     int32_t T, E, top, groups, top_groups, group_top;
     int32_t per_group, stretch;  // experts of a group, tokens of a workgroup
@@ -111,7 +111,32 @@ __device__ __forceinline__ F route_sum(F x)
 }
 
 __device__ __forceinline__ float route_exp(float x) { return expf(x); }
-__device__ __forceinline__ double route_exp(double x) { return exp(x); }
+// e^x in binary64 to about one step: x = n log 2 + r, |r| <= 0.35, Taylor's series of e^r
+// to r^13 (the next term is 5e-18), times 2^n; log 2 in two parts, the first of 32 bits, so
+// that n times it is exact.  A third of the library function's instructions.
+__device__ __forceinline__ double route_exp(double x)
+{
+    const double n = __builtin_rint(fmin(fmax(x, -1100.), 1100.) * 1.4426950408889634);
+    const double r = __builtin_fma(n, -1.9082149292705877e-10, __builtin_fma(n, -0.6931471803691238, x));
+    double p = 1. / 6227020800.;
+    const double c[13] = {1. / 479001600., 1. / 39916800., 1. / 3628800., 1. / 362880., 1. / 40320., 1. / 5040., 1. / 720.,
+                          1. / 120.,       1. / 24.,       1. / 6.,       0.5,          1.,          1.};
+#pragma unroll
+    for (int i = 0; i < 13; ++i) p = __builtin_fma(p, r, c[i]);
+    // beyond the range the exponent decides (r may be anything there); NaN stays
+    const double y = __builtin_ldexp(p, (int)n);
+    return x > 710. ? __builtin_inf() : x < -746. ? 0. : y;
+}
+
+__device__ __forceinline__ float route_inverse(float x) { return 1.f / x; }
+// 1 / x for x >= 1, or x = inf: two Newton steps from the instruction's estimate.
+__device__ __forceinline__ double route_inverse(double x)
+{
+    double y = __builtin_amdgcn_rcp(x);
+    y = __builtin_fma(__builtin_fma(-x, y, 1.), y, y);
+    y = __builtin_fma(__builtin_fma(-x, y, 1.), y, y);
+    return x > 1.7e308 ? 0. : y;
+}
 
 template <bool WIDE>
 struct RouteTypes {
@@ -124,26 +149,40 @@ struct RouteTypes<true> {
     typedef uint64_t Key;
 };
 
-// The experts of token t: lane k < top ends with expert k (-1: none) and its weight.
-// `room`: E doubles of the wave's own in LDS, where groups are left out.
-template <int IN, int V, bool WIDE>
-__device__ __forceinline__ void route_token(const RouteArgs &g, int64_t t, const int (&group)[V], const float (&bias)[V], double *room, int &expert,
-                                            float &weight)
+// The value that a key of binary64 stands for.
+__device__ __forceinline__ double route_value(uint64_t key) { return __longlong_as_double((int64_t)(key >> 63 ? key ^ 1ull << 63 : ~key)); }
+
+// Neighbouring V elements of a row from lane V on, -inf past it.
+template <int IN, int V>
+__device__ __forceinline__ void route_row(const void *x, int64_t at, int left, float (&v)[V])
+{
+    if (left >= V) {
+        typename std::conditional<IN == OUT_F32, uint32_t, uint16_t>::type u[V];
+        __builtin_memcpy(u, static_cast<const uint8_t *>(x) + at * (int64_t)sizeof(u[0]), sizeof(u));  // global memory takes any alignment
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v[i] = IN == OUT_F32    ? __uint_as_float((uint32_t)u[i])
+                   : IN == OUT_BF16 ? __uint_as_float((uint32_t)u[i] << 16)
+                                    : (float)__builtin_bit_cast(_Float16, (uint16_t)u[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = i < left ? route_load<IN>(x, at + i) : -__builtin_inff();
+    }
+}
+
+// The experts of a token with logits x: lane k < top ends with expert k (-1: none) and its
+// weight.  `room`: E doubles of the wave's own in LDS, for groups that are not whole lanes.
+template <int V, bool WIDE>
+__device__ __forceinline__ void route_token(const RouteArgs &g, const float (&x)[V], const float (&bias)[V], double *room, int &expert, float &weight)
 {
     typedef typename RouteTypes<WIDE>::F F;
     typedef typename RouteTypes<WIDE>::Key Key;
     const int lane = threadIdx.x & 63;
-    float x[V];
     const float none = -__builtin_inff();
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = lane * V + i;
-        x[i] = e < g.E ? route_load<IN>(g.logits, t * g.ldl + e) : none;
-    }
-    F p[V], total = 1;
+    F p[V], inverse = 1;
     if (g.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = x[i] == none ? (F)0 : (F)1 / ((F)1 + route_exp(-(F)x[i]));
+        for (int i = 0; i < V; ++i) p[i] = x[i] == none ? (F)0 : route_inverse((F)1 + route_exp(-(F)x[i]));
     } else {
         uint32_t best = 0;
 #pragma unroll
@@ -156,78 +195,98 @@ __device__ __forceinline__ void route_token(const RouteArgs &g, int64_t t, const
             p[i] = x[i] == none ? (F)0 : route_exp((F)x[i] - (F)most);
             sum += p[i];
         }
-        total = route_sum(sum);
+        inverse = route_inverse(route_sum(sum));  // the largest alone is 1
     }
     Key key[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if (WIDE) {
-            const F c = (g.sigmoid ? p[i] : p[i] / total) + (F)bias[i];
-            key[i] = (Key)(x[i] == none ? 0 : route_key(c));
-        } else {
-            key[i] = (Key)route_key(x[i]);
-        }
-    }
+    for (int i = 0; i < V; ++i)
+        key[i] = WIDE ? (Key)(x[i] == none ? 0 : route_key(p[i] * inverse + (F)bias[i])) : (Key)route_key(x[i]);
     if (g.top_groups < g.groups) {
-        // lane j scores group j
+        const int lanes = g.per_group / V;
+        if (lanes * V == g.per_group && (lanes & (lanes - 1)) == 0) {
+            // a group is `lanes` neighbouring lanes: its two largest keys meet in all of them
+            Key k1 = key[0], k2 = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane * V + i;
-            const F c = WIDE ? (g.sigmoid ? p[i] : p[i] / total) + (F)bias[i] : (F)x[i];
-            if (e < g.E) room[e] = x[i] == none ? -__builtin_inf() : (double)c;
-        }
-        __builtin_amdgcn_wave_barrier();
-        double first = -__builtin_inf(), second = first;
-        uint64_t k1 = 0, k2 = 0;
-        if (lane < g.groups)
-            for (int j = 0; j < g.per_group; ++j) {
-                const double c = room[lane * g.per_group + j];
-                const uint64_t k = route_key(c);
-                if (k > k1) {
-                    second = first, k2 = k1;
-                    first = c, k1 = k;
-                } else if (k > k2) {
-                    second = c, k2 = k;
-                }
+            for (int i = 1; i < V; ++i) {
+                k2 = max(k2, min(k1, key[i]));
+                k1 = max(k1, key[i]);
             }
-        const uint64_t score = k1 == 0 ? 0 : route_key(g.group_top > 1 && k2 != 0 ? first + second : first);
-        int better = 0;
-        for (int j = 0; j < g.groups; ++j) {
-            const uint64_t other = route_readlane(score, j);
-            better += other > score || (other == score && j < lane) ? 1 : 0;
+            for (int d = 1; d < lanes; d *= 2) {
+                const Key o1 = (Key)__shfl_xor((unsigned long long)k1, d), o2 = (Key)__shfl_xor((unsigned long long)k2, d);
+                k2 = max(max(k2, o2), min(k1, o1));
+                k1 = max(k1, o1);
+            }
+            // sums are of binary64 scores; one score, as its key
+            const uint64_t score = WIDE && g.group_top > 1 && k1 != 0 && k2 != 0 ? route_key(route_value(k1) + route_value(k2)) : (uint64_t)k1;
+            const int mine = lane / lanes;
+            int better = 0;
+            for (int j = 0; j < g.groups; ++j) {
+                const uint64_t other = route_readlane(score, j * lanes);
+                better += other > score || (other == score && j < mine) ? 1 : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) key[i] = better < g.top_groups ? key[i] : 0;
+        } else {
+            // lane j scores group j
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = lane * V + i;
+                if (e < g.E) reinterpret_cast<uint64_t *>(room)[e] = key[i];
+            }
+            __builtin_amdgcn_wave_barrier();
+            uint64_t k1 = 0, k2 = 0;
+            if (lane < g.groups)
+                for (int j = 0; j < g.per_group; ++j) {
+                    const uint64_t k = reinterpret_cast<const uint64_t *>(room)[lane * g.per_group + j];
+                    k2 = max(k2, min(k1, k));
+                    k1 = max(k1, k);
+                }
+            const uint64_t score = WIDE && g.group_top > 1 && k1 != 0 && k2 != 0 ? route_key(route_value(k1) + route_value(k2)) : k1;
+            int better = 0;
+            for (int j = 0; j < g.groups; ++j) {
+                const uint64_t other = route_readlane(score, j);
+                better += other > score || (other == score && j < lane) ? 1 : 0;
+            }
+            const uint64_t kept = __ballot(lane < g.groups && better < g.top_groups);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = lane * V + i;
+                key[i] = e < g.E && (kept >> (e / g.per_group) & 1) ? key[i] : 0;
+            }
+            __builtin_amdgcn_wave_barrier();
         }
-        const uint64_t kept = __ballot(lane < g.groups && better < g.top_groups);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (!(kept >> group[i] & 1)) key[i] = 0;
-        __builtin_amdgcn_wave_barrier();
     }
+    // each lane's best in turn; lane k takes the k-th
     expert = -1;
-    F mine = 0, chosen = 0;
-    for (int k = 0; k < g.top; ++k) {
-        Key best = key[0];
-        int at = 0;
+    Key best = key[0];
+    int at = 0;
 #pragma unroll
-        for (int i = 1; i < V; ++i)
-            if (key[i] > best) best = key[i], at = i;
+    for (int i = 1; i < V; ++i)
+        if (key[i] > best) best = key[i], at = i;
+    for (int k = 0; k < g.top; ++k) {
         const int from = __builtin_amdgcn_readfirstlane(route_first(best));
         if (from < 0) break;
-        F q = p[0];
-#pragma unroll
-        for (int i = 1; i < V; ++i) q = at == i ? p[i] : q;
-        q = route_readlane(q, from);
-        chosen += q;
         const int e = from * V + __builtin_amdgcn_readlane(at, from);  // by all lanes: a branch would leave others' registers
-        if (lane == k) {
-            expert = e;
-            mine = q;
-        }
+        expert = lane == k ? e : expert;
+        if (lane == from) {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (lane == from && at == i) key[i] = 0;
+            for (int i = 0; i < V; ++i) key[i] = at == i ? 0 : key[i];
+            best = key[0];
+            at = 0;
+#pragma unroll
+            for (int i = 1; i < V; ++i)
+                if (key[i] > best) best = key[i], at = i;
+        }
     }
-    if (g.renormalise) total = chosen == 0 ? (F)1 : chosen;
-    weight = expert < 0 ? 0.f : (float)((F)g.scale * (mine / total));
+    // their scores, from the lanes that hold them
+    F mine = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const F q = __shfl(p[i], max(expert, 0) / V);
+        mine = expert >= 0 && expert % V == i ? q : mine;
+    }
+    const F chosen = g.renormalise ? route_sum(mine) : (F)0;
+    weight = expert < 0 ? 0.f : (float)((F)g.scale * (g.renormalise ? (chosen == 0 ? (F)0 : mine / chosen) : mine * inverse));
 }
 
 // Exclusive sums of n <= 1024 counts in LDS over a workgroup's threads; sums[n] the whole.
@@ -244,30 +303,19 @@ __device__ __forceinline__ void route_offsets(const int32_t *count, int32_t *sum
     __syncthreads();
 }
 
-// The places of a workgroup's tokens [t0, t1), whose ranks among their expert's the
-// first kernel left there, and the rows' tokens; base[e]: where this workgroup's begin.
-__device__ __forceinline__ void route_place(const RouteArgs &g, int64_t t0, int64_t t1, const int32_t *base)
-{
-    for (int64_t i = t0 * g.top + threadIdx.x; i < t1 * g.top; i += kRouteThreads) {
-        const int e = g.experts[i];
-        if (e < 0) continue;  // its place is -1 already
-        const int at = base[e] + g.places[i];
-        g.places[i] = at;
-        g.rows[at] = (int32_t)(i / g.top);
-    }
-}
-
 // Rows behind the last expert's are nobody's.
 __device__ __forceinline__ void route_tail(const RouteArgs &g, int used, int block, int blocks)
 {
     for (int64_t i = used + (int64_t)block * kRouteThreads + threadIdx.x; i < (int64_t)g.T * g.top; i += (int64_t)blocks * kRouteThreads) g.rows[i] = -1;
 }
 
+__host__ __device__ inline int route_pitch(int E) { return (E + 1) & ~1; }
+
 // LDS: masks [E][2], counts [E], sums [E + 1], part [waves]; room [waves][E] doubles.
 __host__ __device__ inline int route_lds(int E, bool groups) { return ((4 * (4 * E + 1 + kRouteWaves) + 7) & ~7) + (groups ? 8 * kRouteWaves * E : 0); }
 
-// Chooses every token's experts; with one workgroup (`alone`) the lists too, else each
-// workgroup's counts.  PER: tokens of a wave in a round.
+// Chooses every token's experts; with one workgroup (`alone`, one round) the lists too,
+// else each workgroup's counts.  `per`: tokens of a wave in a round.
 template <int IN, int V, bool WIDE>
 __global__ __launch_bounds__(kRouteThreads) void route_choose_kernel(RouteArgs g, int per, int alone)
 {
@@ -276,48 +324,46 @@ __global__ __launch_bounds__(kRouteThreads) void route_choose_kernel(RouteArgs g
     int32_t *count = reinterpret_cast<int32_t *>(mask + 2 * g.E), *sums = count + g.E, *part = sums + g.E + 1;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     double *room = reinterpret_cast<double *>(smem + route_lds(g.E, false)) + wave * g.E;
-    int group[V];
-    float bias[V];
+    const int64_t t0 = (int64_t)blockIdx.x * g.stretch, t1 = min((int64_t)g.T, t0 + g.stretch);
+    const int left = g.E - lane * V;
+    float x[V], bias[V];
+    auto load = [&](int64_t t) __attribute__((always_inline)) { route_row<IN, V>(g.logits, t * g.ldl + lane * V, left, x); };
+    if (t0 + wave * per < t1) load(t0 + wave * per);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = lane * V + i;
-        group[i] = e < g.E ? e / g.per_group : 0;
-        bias[i] = WIDE && g.bias != nullptr && e < g.E ? g.bias[e] : 0.f;
-    }
+    for (int i = 0; i < V; ++i) bias[i] = WIDE && g.bias != nullptr && i < left ? g.bias[lane * V + i] : 0.f;
     for (int i = tid; i < g.E; i += kRouteThreads) {
         count[i] = 0;
         mask[2 * i] = mask[2 * i + 1] = 0;
     }
     __syncthreads();
-    const int64_t t0 = (int64_t)blockIdx.x * g.stretch, t1 = min((int64_t)g.T, t0 + g.stretch);
     for (int64_t r0 = t0; r0 < t1; r0 += kRouteWaves * per) {
         int chosen[4];
+        float weight[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             chosen[j] = -1;
             const int local = wave * per + j;
             const int64_t t = r0 + local;
             if (j >= per || t >= t1) continue;
-            float weight;
-            route_token<IN, V, WIDE>(g, t, group, bias, room, chosen[j], weight);
-            if (lane < g.top) {
-                g.experts[t * g.top + lane] = chosen[j];
-                g.weights[t * g.top + lane] = weight;
-                if (chosen[j] >= 0) atomicOr(&mask[2 * chosen[j] + (local >> 5)], 1u << (local & 31));
-            }
+            float now[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) now[i] = x[i];
+            // the next token's logits are on their way meanwhile
+            const int64_t next = j + 1 < per ? t + 1 : t + 1 - per + kRouteWaves * per;
+            if (next < t1) load(next);
+            route_token<V, WIDE>(g, now, bias, room, chosen[j], weight[j]);
+            if (lane < g.top && chosen[j] >= 0) atomicOr(&mask[2 * chosen[j] + (local >> 5)], 1u << (local & 31));
         }
         __syncthreads();
+        int rank[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int local = wave * per + j;
-            const int64_t t = r0 + local;
-            if (j >= per || t >= t1 || lane >= g.top) continue;
-            int rank = -1;
+            rank[j] = -1;
             if (chosen[j] >= 0) {
                 const uint64_t m = (uint64_t)mask[2 * chosen[j] + 1] << 32 | mask[2 * chosen[j]];
-                rank = count[chosen[j]] + (int)__popcll(m & ((1ull << local) - 1));
+                rank[j] = count[chosen[j]] + (int)__popcll(m & ((1ull << local) - 1));
             }
-            g.places[t * g.top + lane] = rank;
         }
         __syncthreads();
         for (int i = tid; i < g.E; i += kRouteThreads) {
@@ -325,15 +371,27 @@ __global__ __launch_bounds__(kRouteThreads) void route_choose_kernel(RouteArgs g
             mask[2 * i] = mask[2 * i + 1] = 0;
         }
         __syncthreads();
+        if (alone) {
+            route_offsets(count, sums, g.E, part);
+            for (int i = tid; i <= g.E; i += kRouteThreads) g.offsets[i] = sums[i];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t t = r0 + wave * per + j;
+            if (j >= per || t >= t1 || lane >= g.top) continue;
+            if (alone && chosen[j] >= 0) {
+                rank[j] += sums[chosen[j]];
+                g.rows[rank[j]] = (int32_t)t;
+            }
+            g.experts[t * g.top + lane] = chosen[j];
+            g.weights[t * g.top + lane] = weight[j];
+            g.places[t * g.top + lane] = rank[j];
+        }
     }
-    if (!alone) {
-        for (int i = tid; i < g.E; i += kRouteThreads) g.counts[(int64_t)blockIdx.x * g.E + i] = count[i];
-        return;
-    }
-    route_offsets(count, sums, g.E, part);
-    for (int i = tid; i <= g.E; i += kRouteThreads) g.offsets[i] = sums[i];
-    route_place(g, t0, t1, sums);  // its own writes of this workgroup, behind barriers
-    route_tail(g, sums[g.E], 0, 1);
+    if (alone)
+        route_tail(g, sums[g.E], 0, 1);
+    else
+        for (int i = tid; i < g.E; i += kRouteThreads) g.counts[(int64_t)blockIdx.x * route_pitch(g.E) + i] = (uint16_t)count[i];
 }
 
 // The lists from the workgroups' counts: each adds up those of the ones before it.
@@ -343,19 +401,41 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs g)
     // before [E], total [E], sums [E + 1], part [waves]
     int32_t *before = reinterpret_cast<int32_t *>(smem), *total = before + g.E, *sums = total + g.E, *part = sums + g.E + 1;
     const int tid = threadIdx.x, blocks = (int)gridDim.x, mine = (int)blockIdx.x;
+    const int64_t t0 = (int64_t)mine * g.stretch, t1 = min((int64_t)g.T, t0 + g.stretch);
+    // the first of this thread's entries are on their way meanwhile
+    const int64_t own = t0 * g.top + tid;
+    int expert = -1, rank = 0;
+    if (own < t1 * g.top) {
+        expert = g.experts[own];
+        rank = g.places[own];
+    }
     for (int i = tid; i < g.E; i += kRouteThreads) before[i] = total[i] = 0;
     __syncthreads();
-    const int lanes = min(kRouteThreads, (g.E + 63) / 64 * 64), parts = kRouteThreads / lanes;
-    const int e = tid % lanes, first = tid / lanes;
+    // two experts a thread, every `parts`-th workgroup
+    const int pitch = route_pitch(g.E), lanes = min(kRouteThreads, (pitch / 2 + 63) / 64 * 64), parts = kRouteThreads / lanes;
+    const int e = tid % lanes * 2, first = tid / lanes;
     if (e < g.E && first < parts) {
-        int b = 0, a = 0;
-        for (int i = first; i < blocks; i += parts) {
-            const int c = g.counts[(int64_t)i * g.E + e];
-            a += c;
-            b += i < mine ? c : 0;
+        int b0 = 0, a0 = 0, b1 = 0, a1 = 0;
+        for (int i = first; i < blocks; i += 16 * parts) {
+            uint32_t c[16];  // on their way together
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                c[j] = i + j * parts < blocks ? *reinterpret_cast<const uint32_t *>(g.counts + (int64_t)(i + j * parts) * pitch + e) : 0u;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const bool earlier = i + j * parts < mine;
+                a0 += c[j] & 0xFFFFu;
+                a1 += c[j] >> 16;
+                b0 += earlier ? c[j] & 0xFFFFu : 0u;
+                b1 += earlier ? c[j] >> 16 : 0u;
+            }
         }
-        atomicAdd(&total[e], a);  // whole numbers: any order
-        atomicAdd(&before[e], b);
+        atomicAdd(&total[e], a0);  // whole numbers: any order
+        atomicAdd(&before[e], b0);
+        if (e + 1 < g.E) {  // an odd number's last half holds nothing
+            atomicAdd(&total[e + 1], a1);
+            atomicAdd(&before[e + 1], b1);
+        }
     }
     __syncthreads();
     route_offsets(total, sums, g.E, part);
@@ -363,8 +443,16 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs g)
     if (mine == 0)
         for (int i = tid; i <= g.E; i += kRouteThreads) g.offsets[i] = sums[i];
     __syncthreads();
-    const int64_t t0 = (int64_t)mine * g.stretch, t1 = min((int64_t)g.T, t0 + g.stretch);
-    route_place(g, t0, t1, before);
+    for (int64_t i = own; i < t1 * g.top; i += kRouteThreads) {
+        if (i != own) {
+            expert = g.experts[i];
+            rank = g.places[i];
+        }
+        if (expert < 0) continue;  // its place is -1 already
+        const int at = before[expert] + rank;
+        g.places[i] = at;
+        g.rows[at] = (int32_t)(i / g.top);
+    }
     route_tail(g, sums[g.E], mine, blocks);
 }
 
@@ -389,15 +477,6 @@ struct RouteGradArgs {
     float scale;
 };
 
-template <int OUT>
-__device__ __forceinline__ void route_store(void *y, int64_t at, float x)
-{
-    if (OUT == OUT_F32)
-        static_cast<float *>(y)[at] = x;
-    else
-        static_cast<uint16_t *>(y)[at] = (uint16_t)(mx_pack2<OUT>(x, 0.f) & 0xFFFFu);
-}
-
 template <int IN, int V>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs g)
 {
@@ -408,12 +487,19 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs g)
     float p[V], slope[V];  // p and, for sigmoid, p (1 - p)
     float total = 1.f, most = 0.f;
     if (!g.sigmoid) most = none;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = lane * V + i;
-        p[i] = e < g.E ? route_load<IN>(g.logits, t * g.ldl + e) : none;
-        if (!g.sigmoid) most = p[i] > most || p[i] != p[i] ? p[i] : most;
+    // lane k's expert, weight's gradient and logit are on their way beside the row
+    int e = -1;
+    float d = 0.f, own = none;
+    if (lane < g.top) {
+        e = g.experts[t * g.top + lane];
+        d = g.dweights[t * g.top + lane];
     }
+    route_row<IN, V>(g.logits, t * g.ldl + lane * V, g.E - lane * V, p);
+    if (e < 0 || e >= g.E) e = -1;
+    if (e >= 0) own = route_load<IN>(g.logits, t * g.ldl + e);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (!g.sigmoid) most = p[i] > most || p[i] != p[i] ? p[i] : most;
     if (!g.sigmoid) {
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
@@ -439,17 +525,13 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs g)
             slope[i] = p[i] /= total;
         }
     }
-    // lane k: expert k, its p and its weight's gradient
-    int e = -1;
-    float q = 0.f, d = 0.f;
-    if (lane < g.top) {
-        e = g.experts[t * g.top + lane];
-        if (e < 0 || e >= g.E) e = -1;
-        if (e >= 0) {
-            const float x = route_load<IN>(g.logits, t * g.ldl + e);
-            q = g.sigmoid ? sigmoid(x) : x == none ? 0.f : expf(x - most) / total;
-            d = g.scale * g.dweights[t * g.top + lane];
-        }
+    // lane k: expert k's p, and its weight's gradient times the scale
+    float q = 0.f;
+    if (e >= 0) {
+        q = g.sigmoid ? sigmoid(own) : own == none ? 0.f : expf(own - most) / total;
+        d *= g.scale;
+    } else {
+        d = 0.f;
     }
     if (g.renormalise) {
         const float S = route_sum(q), mean = route_sum(d * q);
@@ -466,10 +548,21 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs g)
     }
     float mean = 0.f;
     if (!g.sigmoid && !g.renormalise) mean = route_sum(e >= 0 ? q * d : 0.f);
+    const int left = g.E - lane * V;
+    typename std::conditional<IN == OUT_F32, float, uint16_t>::type out[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int to = lane * V + i;
-        if (to < g.E) route_store<IN>(g.dlogits, t * g.E + to, slope[i] * (dp[i] - mean));
+        const float x = slope[i] * (dp[i] - mean);
+        if constexpr (IN == OUT_F32) out[i] = x;
+        else out[i] = (uint16_t)(mx_pack2<IN>(x, 0.f) & 0xFFFFu);
+    }
+    auto *to = static_cast<decltype(&out[0])>(g.dlogits) + t * g.E + lane * V;
+    if (left >= V) {
+        __builtin_memcpy(to, out, sizeof(out));  // global memory takes any alignment
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < left) to[i] = out[i];
     }
 }
 
@@ -493,15 +586,7 @@ __device__ __forceinline__ void route_load8(const void *x, int64_t at, int left,
     u32x4 w[2];
     mx_load8<IN, false>(x, at, left, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (IN == OUT_F32) {
-            v[j] = __uint_as_float(w[j / 4][j % 4]);
-        } else {
-            const uint32_t d = w[0][j / 2];
-            if (IN == OUT_BF16) v[j] = __uint_as_float(j % 2 ? d & 0xFFFF0000u : d << 16);
-            else v[j] = (float)__builtin_bit_cast(_Float16, (uint16_t)(j % 2 ? d >> 16 : d));
-        }
-    }
+    for (int j = 0; j < 8; ++j) v[j] = f8_element<IN>(w, j);
 }
 template <int OUT>
 __device__ __forceinline__ void route_store8(void *y, int64_t at, int n, int N, const float (&v)[8])
@@ -510,36 +595,52 @@ __device__ __forceinline__ void route_store8(void *y, int64_t at, int n, int N, 
     mx_store4<OUT>(y, at, n + 4, N, v[4], v[5], v[6], v[7]);
 }
 
-template <int IN, int OUT>
+// A workgroup takes J pieces of 2048 values of a row.
+template <int IN, int OUT, int J>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs g)
 {
     const int64_t t = blockIdx.x / g.pieces;
-    const int n = (int)(blockIdx.x % g.pieces) * 2048 + 8 * (int)threadIdx.x;
-    if (n >= g.N) return;
-    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, v[4][8];
+    const int n0 = (int)(blockIdx.x % g.pieces) * (2048 * J) + 8 * (int)threadIdx.x;
+    float sum[J][8];
+#pragma unroll
+    for (int q = 0; q < J; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[q][i] = 0.f;
     for (int k0 = 0; k0 < g.top; k0 += 4) {
         float w[4];
-        bool there[4];
+        int at[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int k = k0 + j;
-            const int at = k < g.top ? g.places[t * g.top + k] : -1;
-            there[j] = at >= 0 && at < g.R;
-            w[j] = there[j] && g.weights != nullptr ? g.weights[t * g.top + k] : 1.f;
-            if (there[j]) route_load8<IN>(g.y, (int64_t)at * g.N + n, g.N - n, v[j]);
+            at[j] = k < g.top ? g.places[t * g.top + k] : -1;
+            w[j] = k < g.top && g.weights != nullptr ? g.weights[t * g.top + k] : 1.f;
+            if (at[j] >= g.R) at[j] = -1;
         }
+        u32x4 v[J][4][2];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (there[j])
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(w[j], v[j][i], sum[i]);
-    }
-    if (g.residual != nullptr) {
-        route_load8<OUT>(g.residual, t * g.N + n, g.N - n, v[0]);
+            for (int q = 0; q < J; ++q)
+                if (at[j] >= 0) mx_load8<IN, false>(g.y, (int64_t)at[j] * g.N + n0 + 2048 * q, g.N - n0 - 2048 * q, v[q][j]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] += v[0][i];
+        for (int j = 0; j < 4; ++j)
+            if (at[j] >= 0)
+#pragma unroll
+                for (int q = 0; q < J; ++q)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum[q][i] = __builtin_fmaf(w[j], f8_element<IN>(v[q][j], i), sum[q][i]);
     }
-    route_store8<OUT>(g.out, t * g.N, n, g.N, sum);
+#pragma unroll
+    for (int q = 0; q < J; ++q) {
+        const int n = n0 + 2048 * q;
+        if (g.residual != nullptr) {
+            u32x4 v[2];
+            mx_load8<OUT, false>(g.residual, t * g.N + n, g.N - n, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[q][i] += f8_element<OUT>(v, i);
+        }
+        route_store8<OUT>(g.out, t * g.N, n, g.N, sum[q]);
+    }
 }
 
 // dy[places[t][k]] = weights[t][k] dout[t];  dweights[t][k] = <dout[t], y[places[t][k]]>.

@@ -7,8 +7,8 @@ using namespace lpgemm;
 
 namespace {
 
-// Tokens are dealt to this many workgroups at most: every one of the second kernel adds
-// up the counts of the others.
+// Tokens are dealt to this many workgroups (beyond 16 million, to more): every one of the
+// second kernel adds up the counts of the others.
 constexpr int64_t kMostWorkgroups = 256;
 
 // How T tokens are dealt: tokens of a wave in a round, of a workgroup, workgroups.
@@ -18,8 +18,9 @@ struct RoutePlan {
 };
 RoutePlan plan_route(int64_t T)
 {
-    const int per = T <= kRouteWaves * kMostWorkgroups ? 1 : 4;
-    const int64_t round = (int64_t)kRouteWaves * per, stretch = round * ceil_div(ceil_div(T, round), kMostWorkgroups);
+    const int per = T <= kRouteWaves * kMostWorkgroups ? 1 : T <= 2 * kRouteWaves * kMostWorkgroups ? 2 : 4;
+    const int64_t round = (int64_t)kRouteWaves * per, rounds = ceil_div(ceil_div(T, round), kMostWorkgroups);
+    const int64_t stretch = round * std::min<int64_t>(rounds, UINT16_MAX / round);  // counts of 16 bits
     return {per, stretch, ceil_div(T, stretch)};
 }
 
@@ -27,7 +28,7 @@ size_t route_workspace(int64_t T, int64_t E)
 {
     if (T == 0 || E == 0) return 0;
     const RoutePlan p = plan_route(T);
-    return p.blocks > 1 ? (size_t)(p.blocks * E) * sizeof(int32_t) : 0;
+    return p.blocks > 1 ? (size_t)(p.blocks * route_pitch((int)E)) * sizeof(uint16_t) : 0;
 }
 
 lpgemm_status check_options(const lpgemm_route_options *o, int64_t T, int64_t E, int64_t ld)
@@ -97,9 +98,13 @@ lpgemm_status launch_backward(const RouteGradArgs &g, hipStream_t stream)
 }
 
 template <int IN>
-lpgemm_status launch_combine(const CombineArgs &g, int out, hipStream_t stream)
+lpgemm_status launch_combine(CombineArgs g, int out, hipStream_t stream)
 {
-    const auto kernel = out == OUT_F32 ? &combine_kernel<IN, OUT_F32> : out == OUT_BF16 ? &combine_kernel<IN, OUT_BF16> : &combine_kernel<IN, OUT_F16>;
+    const bool two = g.N > 2048 && g.T >= 1024;  // long rows of many tokens: more loads in flight
+    const auto kernel = out == OUT_F32    ? two ? &combine_kernel<IN, OUT_F32, 2> : &combine_kernel<IN, OUT_F32, 1>
+                        : out == OUT_BF16 ? two ? &combine_kernel<IN, OUT_BF16, 2> : &combine_kernel<IN, OUT_BF16, 1>
+                                          : two ? &combine_kernel<IN, OUT_F16, 2> : &combine_kernel<IN, OUT_F16, 1>;
+    g.pieces = (int32_t)ceil_div(g.N, two ? 4096 : 2048);
     return launch_rows(g.T, g.pieces, 1, [&](int64_t first, int64_t, dim3 blocks) {
         CombineArgs a = g;
         const int64_t w = out == OUT_F32 ? 4 : 2;
@@ -164,7 +169,7 @@ lpgemm_status lpgemm_route(const void *logits, lpgemm_out_dtype dtype, int64_t l
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 4))) return LPGEMM_ERR_INVALID_ARG;
     (void)hipGetLastError();
     const lpgemm_route_options &o = *options;
-    const RouteArgs g{logits, bias, experts, weights, rows, offsets, places, static_cast<int32_t *>(workspace), ldl, (int32_t)T, (int32_t)E, o.top, o.groups,
+    const RouteArgs g{logits, bias, experts, weights, rows, offsets, places, static_cast<uint16_t *>(workspace), ldl, (int32_t)T, (int32_t)E, o.top, o.groups,
                       o.top_groups, o.group_top, (int32_t)std::max<int64_t>(1, E / o.groups), (int32_t)(T > 0 ? plan_route(T).stretch : 0),
                       o.score == LPGEMM_ROUTE_SIGMOID, o.renormalise, o.scale};
     if (T == 0) {
@@ -209,7 +214,7 @@ lpgemm_status lpgemm_combine(const void *Y, lpgemm_out_dtype y_dtype, int64_t R,
         !aligned(weights, 4) || !aligned(residual, element_bytes(o)) || !aligned(out, element_bytes(o)))
         return LPGEMM_ERR_INVALID_ARG;
     (void)hipGetLastError();
-    const CombineArgs g{Y, places, weights, residual, out, R, T, (int32_t)N, (int32_t)top, (int32_t)ceil_div(N, 2048)};
+    const CombineArgs g{Y, places, weights, residual, out, R, T, (int32_t)N, (int32_t)top, 1};
     switch (f) {
     case OUT_F32: return launch_combine<OUT_F32>(g, o, stream);
     case OUT_BF16: return launch_combine<OUT_BF16>(g, o, stream);
