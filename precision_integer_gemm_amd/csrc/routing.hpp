@@ -46,18 +46,19 @@ __device__ __forceinline__ float route_load(const void *x, int64_t at)
     return (float)__builtin_bit_cast(_Float16, u);
 }
 
-// Unsigned keys that order as the values do: NaN above all, -0 as 0; 0 stands for closed.
+// Unsigned keys that order as the values do: NaN above all, -0 as 0, -inf 0.  Without
+// branches, which the compiler makes of conditions on conditions.
 __device__ __forceinline__ uint32_t route_key(float x)
 {
-    if (x != x) return 0xFFFFFFFFu;
-    const uint32_t u = __float_as_uint(x + 0.f);
-    return x == -__builtin_inff() ? 0u : (int32_t)u < 0 ? ~u : u | 0x80000000u;
+    const uint32_t u = __float_as_uint(x + 0.f), k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    return (k | (x != x ? ~0u : 0u)) & (x == -__builtin_inff() ? 0u : ~0u);
 }
 __device__ __forceinline__ uint64_t route_key(double x)
 {
-    if (x != x) return ~0ull;
     const uint64_t u = (uint64_t)__double_as_longlong(x + 0.);
-    return x == -__builtin_inf() ? 0ull : (int64_t)u < 0 ? ~u : u | 1ull << 63;
+    const uint32_t sign = (uint32_t)((int32_t)(u >> 32) >> 31), high = x != x ? ~0u : 0u, low = x == -__builtin_inf() ? 0u : ~0u;
+    const uint32_t hi = (((uint32_t)(u >> 32) ^ (sign | 0x80000000u)) | high) & low, lo = (((uint32_t)u ^ sign) | high) & low;
+    return (uint64_t)hi << 32 | lo;
 }
 
 // The largest of all 64 lanes, in all of them.
@@ -110,22 +111,39 @@ __device__ __forceinline__ F route_sum(F x)
     return x;
 }
 
-__device__ __forceinline__ float route_exp(float x) { return expf(x); }
+template <int V>
+__device__ __forceinline__ void route_exp(float (&x)[V])
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = expf(x[i]);
+}
 // e^x in binary64 to about one step: x = n log 2 + r, |r| <= 0.35, Taylor's series of e^r
 // to r^13 (the next term is 5e-18), times 2^n; log 2 in two parts, the first of 32 bits, so
 // that n times it is exact.  A third of the library function's instructions.
-__device__ __forceinline__ double route_exp(double x)
+template <int V>
+__device__ __forceinline__ void route_exp(double (&x)[V])
 {
-    const double n = __builtin_rint(fmin(fmax(x, -1100.), 1100.) * 1.4426950408889634);
-    const double r = __builtin_fma(n, -1.9082149292705877e-10, __builtin_fma(n, -0.6931471803691238, x));
-    double p = 1. / 6227020800.;
+    double r[V], p[V];
+    int n[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const double whole = __builtin_rint(fmin(fmax(x[i], -1100.), 1100.) * 1.4426950408889634);
+        r[i] = __builtin_fma(whole, -1.9082149292705877e-10, __builtin_fma(whole, -0.6931471803691238, x[i]));
+        n[i] = (int)whole;
+        p[i] = 1. / 6227020800.;
+    }
     const double c[13] = {1. / 479001600., 1. / 39916800., 1. / 3628800., 1. / 362880., 1. / 40320., 1. / 5040., 1. / 720.,
                           1. / 120.,       1. / 24.,       1. / 6.,       0.5,          1.,          1.};
 #pragma unroll
-    for (int i = 0; i < 13; ++i) p = __builtin_fma(p, r, c[i]);
+    for (int j = 0; j < 13; ++j) {
+        double k = c[j];
+        asm volatile("" : "+s"(k));  // not 26 registers of every lane through the tokens' loop
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = __builtin_fma(p[i], r[i], k);
+    }
     // beyond the range the exponent decides (r may be anything there); NaN stays
-    const double y = __builtin_ldexp(p, (int)n);
-    return x > 710. ? __builtin_inf() : x < -746. ? 0. : y;
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = x[i] > 710. ? __builtin_inf() : x[i] < -746. ? 0. : __builtin_ldexp(p[i], n[i]);
 }
 
 __device__ __forceinline__ float route_inverse(float x) { return 1.f / x; }
@@ -170,29 +188,40 @@ __device__ __forceinline__ void route_row(const void *x, int64_t at, int left, f
     }
 }
 
-// The experts of a token with logits x: lane k < top ends with expert k (-1: none) and its
-// weight.  `room`: E doubles of the wave's own in LDS, for groups that are not whole lanes.
-template <int V, bool WIDE>
-__device__ __forceinline__ void route_token(const RouteArgs &g, const float (&x)[V], const float (&bias)[V], double *room, int &expert, float &weight)
+// The experts of a token with these logits: lane k < top ends with expert k (-1: none) and
+// its weight.  `room`: E doubles of the wave's own in LDS, for groups that are not whole lanes.
+template <int IN, int V, bool WIDE>
+__device__ __forceinline__ void route_token(const RouteArgs &g, const void *logits, double *room, int &expert, float &weight)
 {
     typedef typename RouteTypes<WIDE>::F F;
     typedef typename RouteTypes<WIDE>::Key Key;
     const int lane = threadIdx.x & 63;
     const float none = -__builtin_inff();
+    const int left = g.E - lane * V;
+    float x[V], bias[V], most = 0.f;
+    route_row<IN, V>(logits, lane * V, left, x);
+#pragma unroll
+    for (int i = 0; i < V; ++i) bias[i] = WIDE && g.bias != nullptr && i < left ? g.bias[lane * V + i] : 0.f;
     F p[V], inverse = 1;
     if (g.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = x[i] == none ? (F)0 : route_inverse((F)1 + route_exp(-(F)x[i]));
+        for (int i = 0; i < V; ++i) p[i] = -(F)x[i];
+        route_exp(p);
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = route_inverse((F)1 + p[i]);  // closed: 1 / inf
     } else {
         uint32_t best = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) best = max(best, route_key(x[i]));
         best = route_largest(best);  // 0: all closed
-        const float most = best == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float((int32_t)best < 0 ? best ^ 0x80000000u : ~best);
+        most = best == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float((int32_t)best < 0 ? best ^ 0x80000000u : ~best);
         F sum = 0;
 #pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = (F)x[i] - (F)most;
+        route_exp(p);
+#pragma unroll
         for (int i = 0; i < V; ++i) {
-            p[i] = x[i] == none ? (F)0 : route_exp((F)x[i] - (F)most);
+            p[i] = x[i] == none ? (F)0 : p[i];  // not NaN where a row's others make it that
             sum += p[i];
         }
         inverse = route_inverse(route_sum(sum));  // the largest alone is 1
@@ -200,7 +229,7 @@ __device__ __forceinline__ void route_token(const RouteArgs &g, const float (&x)
     Key key[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        key[i] = WIDE ? (Key)(x[i] == none ? 0 : route_key(p[i] * inverse + (F)bias[i])) : (Key)route_key(x[i]);
+        key[i] = WIDE ? (Key)route_key(p[i] * inverse + (F)bias[i]) & (x[i] == none ? (Key)0 : ~(Key)0) : (Key)route_key(x[i]);
     if (g.top_groups < g.groups) {
         const int lanes = g.per_group / V;
         if (lanes * V == g.per_group && (lanes & (lanes - 1)) == 0) {
@@ -256,40 +285,60 @@ __device__ __forceinline__ void route_token(const RouteArgs &g, const float (&x)
             __builtin_amdgcn_wave_barrier();
         }
     }
-    // each lane's best in turn; lane k takes the k-th
-    expert = -1;
-    Key best = key[0];
-    int at = 0;
+    // each lane's keys in order, equal ones by index, by an odd-even merging network (Batcher);
+    // their indices, four bits each
+    int index[V];
 #pragma unroll
-    for (int i = 1; i < V; ++i)
-        if (key[i] > best) best = key[i], at = i;
+    for (int i = 0; i < V; ++i) index[i] = i;
+#pragma unroll
+    for (int p = 1; p < V; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < V; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i) {
+                    const int a = i + j, b = i + j + q;
+                    if (b >= V || a / (2 * p) != b / (2 * p)) continue;
+                    const bool swap = key[b] > key[a] || (key[b] == key[a] && index[b] < index[a]);
+                    const Key hi = swap ? key[b] : key[a], lo = swap ? key[a] : key[b];
+                    const int first = swap ? index[b] : index[a], second = swap ? index[a] : index[b];
+                    key[a] = hi, key[b] = lo;
+                    index[a] = first, index[b] = second;
+                }
+    typename std::conditional<(V > 8), uint64_t, uint32_t>::type order = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) order |= (decltype(order))index[i] << (4 * i);
+    // the lanes' best in turn; lane k takes the k-th
+    expert = -1;
     for (int k = 0; k < g.top; ++k) {
-        const int from = __builtin_amdgcn_readfirstlane(route_first(best));
+        const int from = __builtin_amdgcn_readfirstlane(route_first(key[0]));
         if (from < 0) break;
-        const int e = from * V + __builtin_amdgcn_readlane(at, from);  // by all lanes: a branch would leave others' registers
+        const int e = from * V + (__builtin_amdgcn_readlane((int)(uint32_t)order, from) & 15);  // by all lanes: a branch would leave others' registers
         expert = lane == k ? e : expert;
         if (lane == from) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) key[i] = at == i ? 0 : key[i];
-            best = key[0];
-            at = 0;
-#pragma unroll
-            for (int i = 1; i < V; ++i)
-                if (key[i] > best) best = key[i], at = i;
+            for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+            key[V - 1] = 0;
+            order >>= 4;
         }
     }
-    // their scores, from the lanes that hold them
+    // their scores again, by the same steps: kept meanwhile they would take 2 V registers
     F mine = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const F q = __shfl(p[i], max(expert, 0) / V);
-        mine = expert >= 0 && expert % V == i ? q : mine;
+    if (expert >= 0) {
+        const float y = route_load<IN>(logits, expert);
+        F one[1] = {g.sigmoid ? -(F)y : (F)y - (F)most};
+        route_exp(one);
+        mine = g.sigmoid ? route_inverse((F)1 + one[0]) : one[0];
     }
-    const F chosen = g.renormalise ? route_sum(mine) : (F)0;
+    F chosen = mine;
+    if (g.renormalise)
+        for (int d = 1; d < g.top; d *= 2) chosen += __shfl_xor(chosen, d);  // the lanes past the last expert hold 0
     weight = expert < 0 ? 0.f : (float)((F)g.scale * (g.renormalise ? (chosen == 0 ? (F)0 : mine / chosen) : mine * inverse));
 }
 
-// Exclusive sums of n <= 1024 counts in LDS over a workgroup's threads; sums[n] the whole.
+// Exclusive sums of n <= 1024 counts in LDS over a workgroup's threads; sums[n] the whole
+// (the counts may lie there).
 __device__ __forceinline__ void route_offsets(const int32_t *count, int32_t *sums, int n, int32_t *part)
 {
     const int tid = threadIdx.x, wave = tid >> 6;
@@ -311,87 +360,78 @@ __device__ __forceinline__ void route_tail(const RouteArgs &g, int used, int blo
 
 __host__ __device__ inline int route_pitch(int E) { return (E + 1) & ~1; }
 
-// LDS: masks [E][2], counts [E], sums [E + 1], part [waves]; room [waves][E] doubles.
-__host__ __device__ inline int route_lds(int E, bool groups) { return ((4 * (4 * E + 1 + kRouteWaves) + 7) & ~7) + (groups ? 8 * kRouteWaves * E : 0); }
+// A workgroup's tokens in a round: its masks have 64 bits.
+constexpr int kRouteRound = 64;
+
+// LDS: masks [E][2], counts [E], sums [E + 1], part [waves], chosen [round][top] of 16
+// bits; room [waves][E] doubles, where groups are not whole lanes.
+__host__ __device__ inline int route_lds(int E, int top, bool room)
+{
+    return ((4 * (4 * E + 1 + kRouteWaves) + 2 * kRouteRound * top + 7) & ~7) + (room ? 8 * kRouteWaves * E : 0);
+}
 
 // Chooses every token's experts; with one workgroup (`alone`, one round) the lists too,
 // else each workgroup's counts.  `per`: tokens of a wave in a round.
 template <int IN, int V, bool WIDE>
-__global__ __launch_bounds__(kRouteThreads) void route_choose_kernel(RouteArgs g, int per, int alone)
+__global__ __launch_bounds__(kRouteThreads, 4) void route_choose_kernel(RouteArgs g, int per, int alone)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     uint32_t *mask = reinterpret_cast<uint32_t *>(smem);
     int32_t *count = reinterpret_cast<int32_t *>(mask + 2 * g.E), *sums = count + g.E, *part = sums + g.E + 1;
+    int16_t *chosen = reinterpret_cast<int16_t *>(part + kRouteWaves);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    double *room = reinterpret_cast<double *>(smem + route_lds(g.E, false)) + wave * g.E;
+    double *room = reinterpret_cast<double *>(smem + route_lds(g.E, g.top, false)) + wave * g.E;
     const int64_t t0 = (int64_t)blockIdx.x * g.stretch, t1 = min((int64_t)g.T, t0 + g.stretch);
-    const int left = g.E - lane * V;
-    float x[V], bias[V];
-    auto load = [&](int64_t t) __attribute__((always_inline)) { route_row<IN, V>(g.logits, t * g.ldl + lane * V, left, x); };
-    if (t0 + wave * per < t1) load(t0 + wave * per);
-#pragma unroll
-    for (int i = 0; i < V; ++i) bias[i] = WIDE && g.bias != nullptr && i < left ? g.bias[lane * V + i] : 0.f;
     for (int i = tid; i < g.E; i += kRouteThreads) {
         count[i] = 0;
         mask[2 * i] = mask[2 * i + 1] = 0;
     }
     __syncthreads();
     for (int64_t r0 = t0; r0 < t1; r0 += kRouteWaves * per) {
-        int chosen[4];
-        float weight[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            chosen[j] = -1;
-            const int local = wave * per + j;
+        const int tokens = (int)min((int64_t)kRouteWaves * per, t1 - r0);
+        for (int local = wave; local < tokens; local += kRouteWaves) {
             const int64_t t = r0 + local;
-            if (j >= per || t >= t1) continue;
-            float now[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) now[i] = x[i];
-            // the next token's logits are on their way meanwhile
-            const int64_t next = j + 1 < per ? t + 1 : t + 1 - per + kRouteWaves * per;
-            if (next < t1) load(next);
-            route_token<V, WIDE>(g, now, bias, room, chosen[j], weight[j]);
-            if (lane < g.top && chosen[j] >= 0) atomicOr(&mask[2 * chosen[j] + (local >> 5)], 1u << (local & 31));
-        }
-        __syncthreads();
-        int rank[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int local = wave * per + j;
-            rank[j] = -1;
-            if (chosen[j] >= 0) {
-                const uint64_t m = (uint64_t)mask[2 * chosen[j] + 1] << 32 | mask[2 * chosen[j]];
-                rank[j] = count[chosen[j]] + (int)__popcll(m & ((1ull << local) - 1));
+            int expert;
+            float weight;
+            route_token<IN, V, WIDE>(g, static_cast<const uint8_t *>(g.logits) + t * g.ldl * (IN == OUT_F32 ? 4 : 2), room, expert, weight);
+            if (lane < g.top) {
+                g.experts[t * g.top + lane] = expert;
+                g.weights[t * g.top + lane] = weight;
+                chosen[local * g.top + lane] = (int16_t)expert;
+                if (expert >= 0) atomicOr(&mask[2 * expert + (local >> 5)], 1u << (local & 31));
             }
         }
         __syncthreads();
+        // an entry's rank: its expert's earlier rounds and earlier tokens of this one
+        auto rank = [&](int i) __attribute__((always_inline)) -> int {
+            const int e = chosen[i], local = i / g.top;
+            if (e < 0) return -1;
+            const uint64_t m = (uint64_t)mask[2 * e + 1] << 32 | mask[2 * e];
+            return count[e] + (int)__popcll(m & ((1ull << local) - 1));
+        };
+        if (!alone)
+            for (int i = tid; i < tokens * g.top; i += kRouteThreads) g.places[r0 * g.top + i] = rank(i);
+        else if (tid < g.E)
+            sums[tid] = (int)__popc(mask[2 * tid]) + (int)__popc(mask[2 * tid + 1]);
+        __syncthreads();
+        if (alone) {  // counts stay 0: a place is the expert's first row and the rank
+            route_offsets(sums, sums, g.E, part);
+            for (int i = tid; i <= g.E; i += kRouteThreads) g.offsets[i] = sums[i];
+            for (int i = tid; i < tokens * g.top; i += kRouteThreads) {
+                const int at = rank(i);
+                g.places[i] = at < 0 ? -1 : sums[chosen[i]] + at;
+                if (at >= 0) g.rows[sums[chosen[i]] + at] = i / g.top;
+            }
+            route_tail(g, sums[g.E], 0, 1);
+            return;
+        }
         for (int i = tid; i < g.E; i += kRouteThreads) {
             count[i] += (int)__popc(mask[2 * i]) + (int)__popc(mask[2 * i + 1]);
             mask[2 * i] = mask[2 * i + 1] = 0;
         }
         __syncthreads();
-        if (alone) {
-            route_offsets(count, sums, g.E, part);
-            for (int i = tid; i <= g.E; i += kRouteThreads) g.offsets[i] = sums[i];
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t t = r0 + wave * per + j;
-            if (j >= per || t >= t1 || lane >= g.top) continue;
-            if (alone && chosen[j] >= 0) {
-                rank[j] += sums[chosen[j]];
-                g.rows[rank[j]] = (int32_t)t;
-            }
-            g.experts[t * g.top + lane] = chosen[j];
-            g.weights[t * g.top + lane] = weight[j];
-            g.places[t * g.top + lane] = rank[j];
-        }
     }
-    if (alone)
-        route_tail(g, sums[g.E], 0, 1);
-    else
-        for (int i = tid; i < g.E; i += kRouteThreads) g.counts[(int64_t)blockIdx.x * route_pitch(g.E) + i] = (uint16_t)count[i];
+    for (int i = tid; i < g.E; i += kRouteThreads) g.counts[(int64_t)blockIdx.x * route_pitch(g.E) + i] = (uint16_t)count[i];
 }
 
 // The lists from the workgroups' counts: each adds up those of the ones before it.
@@ -400,7 +440,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs g)
     extern __shared__ __align__(16) uint8_t smem[];
     // before [E], total [E], sums [E + 1], part [waves]
     int32_t *before = reinterpret_cast<int32_t *>(smem), *total = before + g.E, *sums = total + g.E, *part = sums + g.E + 1;
-    const int tid = threadIdx.x, blocks = (int)gridDim.x, mine = (int)blockIdx.x;
+    const int tid = threadIdx.x, mine = (int)blockIdx.x, blocks = (int)gridDim.x;
     const int64_t t0 = (int64_t)mine * g.stretch, t1 = min((int64_t)g.T, t0 + g.stretch);
     // the first of this thread's entries are on their way meanwhile
     const int64_t own = t0 * g.top + tid;
@@ -534,7 +574,11 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs g)
         d = 0.f;
     }
     if (g.renormalise) {
-        const float S = route_sum(q), mean = route_sum(d * q);
+        float S = q, mean = d * q;
+        for (int i = 1; i < g.top; i *= 2) {  // the lanes past the last expert hold 0
+            S += __shfl_xor(S, i);
+            mean += __shfl_xor(mean, i);
+        }
         d = S == 0.f ? 0.f : (d - mean / S) / S;
     }
     float dp[V];

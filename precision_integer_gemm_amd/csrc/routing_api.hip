@@ -18,7 +18,8 @@ struct RoutePlan {
 };
 RoutePlan plan_route(int64_t T)
 {
-    const int per = T <= kRouteWaves * kMostWorkgroups ? 1 : T <= 2 * kRouteWaves * kMostWorkgroups ? 2 : 4;
+    int per = 1;
+    while (kRouteWaves * per < kRouteRound && T > kRouteWaves * per * kMostWorkgroups) per *= 2;
     const int64_t round = (int64_t)kRouteWaves * per, rounds = ceil_div(ceil_div(T, round), kMostWorkgroups);
     const int64_t stretch = round * std::min<int64_t>(rounds, UINT16_MAX / round);  // counts of 16 bits
     return {per, stretch, ceil_div(T, stretch)};
@@ -50,9 +51,11 @@ lpgemm_status launch_choose(const RouteArgs &g, const RoutePlan &p, hipStream_t 
     static std::once_flag once[kMaxDevices];
     static hipError_t err[kMaxDevices];
     const auto kernel = &route_choose_kernel<IN, V, WIDE>;
-    const lpgemm_status st = allow_lds(kernel, route_lds(64 * V, true), once, err);
+    const lpgemm_status st = allow_lds(kernel, route_lds(64 * V, LPGEMM_ROUTE_MAX_TOP, true), once, err);
     if (st != LPGEMM_OK) return st;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)p.blocks), dim3(kRouteThreads), route_lds(g.E, g.top_groups < g.groups), stream, g, p.per, p.blocks == 1 ? 1 : 0);
+    const int lanes = g.per_group / V;
+    const bool room = g.top_groups < g.groups && (lanes * V != g.per_group || (lanes & (lanes - 1)) != 0);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)p.blocks), dim3(kRouteThreads), route_lds(g.E, g.top, room), stream, g, p.per, p.blocks == 1 ? 1 : 0);
     return launched();
 }
 
