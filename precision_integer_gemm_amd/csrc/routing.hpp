@@ -639,8 +639,9 @@ __device__ __forceinline__ void route_store8(void *y, int64_t at, int n, int N, 
     mx_store4<OUT>(y, at, n + 4, N, v[4], v[5], v[6], v[7]);
 }
 
-// A workgroup takes J pieces of 2048 values of a row.
-template <int IN, int OUT, int J>
+// A workgroup takes J pieces of 2048 values of a row.  NT: rows that no cache will keep
+// pass by them.
+template <int IN, int OUT, int J, bool NT>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs g)
 {
     const int64_t t = blockIdx.x / g.pieces;
@@ -665,7 +666,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs g)
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int q = 0; q < J; ++q)
-                if (at[j] >= 0) mx_load8<IN, false>(g.y, (int64_t)at[j] * g.N + n0 + 2048 * q, g.N - n0 - 2048 * q, v[q][j]);
+                if (at[j] >= 0) mx_load8<IN, NT>(g.y, (int64_t)at[j] * g.N + n0 + 2048 * q, g.N - n0 - 2048 * q, v[q][j]);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (at[j] >= 0)

@@ -25,6 +25,11 @@ RoutePlan plan_route(int64_t T)
     return {per, stretch, ceil_div(T, stretch)};
 }
 
+// Rows of more bytes than this do not stay in the 256 MB last-level cache between a call
+// and the next: the sum's loads pass by it (8192 x 4 rows of 4096 bf16, 268 MB: 77 us kept,
+// 64 passed by; the gradients, which write as much: 116 and 126, so they are kept).
+constexpr int64_t kPastCaches = 192 << 20;
+
 size_t route_workspace(int64_t T, int64_t E)
 {
     if (T == 0 || E == 0) return 0;
@@ -104,9 +109,14 @@ template <int IN>
 lpgemm_status launch_combine(CombineArgs g, int out, hipStream_t stream)
 {
     const bool two = g.N > 2048 && g.T >= 1024;  // long rows of many tokens: more loads in flight
-    const auto kernel = out == OUT_F32    ? two ? &combine_kernel<IN, OUT_F32, 2> : &combine_kernel<IN, OUT_F32, 1>
-                        : out == OUT_BF16 ? two ? &combine_kernel<IN, OUT_BF16, 2> : &combine_kernel<IN, OUT_BF16, 1>
-                                          : two ? &combine_kernel<IN, OUT_F16, 2> : &combine_kernel<IN, OUT_F16, 1>;
+    const bool past = two && g.R * g.N * (int64_t)element_bytes(IN) > kPastCaches;
+    const auto pick = [&](auto type) {
+        constexpr int OUT = decltype(type)::value;
+        return past ? &combine_kernel<IN, OUT, 2, true> : two ? &combine_kernel<IN, OUT, 2, false> : &combine_kernel<IN, OUT, 1, false>;
+    };
+    const auto kernel = out == OUT_F32    ? pick(std::integral_constant<int, OUT_F32>{})
+                        : out == OUT_BF16 ? pick(std::integral_constant<int, OUT_BF16>{})
+                                          : pick(std::integral_constant<int, OUT_F16>{});
     g.pieces = (int32_t)ceil_div(g.N, two ? 4096 : 2048);
     return launch_rows(g.T, g.pieces, 1, [&](int64_t first, int64_t, dim3 blocks) {
         CombineArgs a = g;
