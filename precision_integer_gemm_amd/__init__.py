@@ -21,7 +21,7 @@ from ._binding import (  # noqa: F401
     lpgemm_mxfp4_workspace_size,
     lpgemm_fp8_block, lpgemm_fp8_block_dequantize, lpgemm_fp8_block_grouped, lpgemm_fp8_block_plan, lpgemm_fp8_block_quantize,
     lpgemm_combine, lpgemm_combine_backward, lpgemm_route, lpgemm_route_backward, lpgemm_route_workspace_size,
-    ROUTE_MAX_EXPERTS, ROUTE_MAX_GROUPS, ROUTE_MAX_TOP, ROUTE_SCORES, Routing,
+    COMBINE_MAX_N, COMBINE_MAX_TOP, ROUTE_MAX_EXPERTS, ROUTE_MAX_GROUPS, ROUTE_MAX_TOP, ROUTE_SCORES, Routing,
     FP8_BLOCK, FP8_BLOCK_MAX_GROUPS, FP8_BLOCK_MAX_K,
     MXFP4_MAX_GROUPS, MXFP4_MAX_K, MXFP4_UNIT, MXFP4_UNIT_CODES, MXFP4_UNIT_SCALES,
     lpgemm_w4a8_blockscaled, lpgemm_w4a8_scaled, lpgemm_workspace_size, SIZE_MAX, STATIC_SCRATCH_BYTES, WORKSPACE_ALIGN)

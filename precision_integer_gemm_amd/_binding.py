@@ -50,6 +50,7 @@ FP8_BLOCK, FP8_BLOCK_MAX_K, FP8_BLOCK_MAX_GROUPS = 128, 1 << 20, 1024
 # lpgemm_route_score, and the routing's limits
 ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
 ROUTE_MAX_EXPERTS, ROUTE_MAX_TOP, ROUTE_MAX_GROUPS = 1024, 32, 64
+COMBINE_MAX_TOP, COMBINE_MAX_N = 1024, 1 << 24
 
 
 class LpgemmError(RuntimeError):

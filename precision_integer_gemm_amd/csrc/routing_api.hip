@@ -43,7 +43,7 @@ lpgemm_status check_options(const lpgemm_route_options *o, int64_t T, int64_t E,
     if ((o->score != LPGEMM_ROUTE_SOFTMAX && o->score != LPGEMM_ROUTE_SIGMOID) || (o->renormalise != 0 && o->renormalise != 1) || o->top < 1 ||
         o->groups < 1 || o->top_groups < 1 || o->top_groups > o->groups || (o->group_top != 1 && o->group_top != 2))
         return LPGEMM_ERR_INVALID_ARG;
-    if (E > LPGEMM_ROUTE_MAX_EXPERTS || o->top > LPGEMM_ROUTE_MAX_TOP || o->groups > LPGEMM_ROUTE_MAX_GROUPS || T * o->top > INT32_MAX)
+    if (E > LPGEMM_ROUTE_MAX_EXPERTS || o->top > LPGEMM_ROUTE_MAX_TOP || o->groups > LPGEMM_ROUTE_MAX_GROUPS || T > INT32_MAX / o->top)
         return LPGEMM_ERR_UNSUPPORTED;
     if (T == 0) return LPGEMM_OK;
     if (E < 1 || E % o->groups != 0 || o->top > E / o->groups * o->top_groups || (T > 1 && (ld < E || ld > (INT64_MAX >> 4) / T))) return LPGEMM_ERR_INVALID_ARG;
