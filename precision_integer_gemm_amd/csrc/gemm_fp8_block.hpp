@@ -362,10 +362,20 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void gemm_fp8_block_tile
 // which the scaling's fused multiply-adds need in plain registers, two waves a SIMD).
 //
 // A stage is one unit (128 k), two slots.  A wave keeps its two blocks of B for the stage
-// and reads its FM blocks of A one ahead; block FM - 1 of a stage is contracted while the
-// next stage's first blocks are read, behind the stage's one barrier: there the next
-// stage has landed, and this one's slot has been read out by all waves and is filled
-// again.  A block's sum is scaled and added while the next block's MFMAs run.
+// and reads its FM blocks of A one ahead.  Block FM - 1 of a stage is contracted while the
+// next stage's first blocks are read, behind a barrier: there the next stage has landed, and
+// this one's A has been read out by all waves and is filled again; its B has been since the
+// second block, behind a barrier of its own.  Copies go out one or two between two blocks of
+// MFMAs all through the stage: 8192^3 takes 475 us with all of them behind the one barrier,
+// 443 with B's behind the other, two at a time, 435 so; asked for half a stage earlier
+// still, but three at a time, 465.  A block's sum is scaled and added while the next
+// block's MFMAs run.
+//
+// Bound by the power that the matrix cores draw and by what the waves wait for at the
+// barriers: 8192^3 435 us (2.53 PFLOP/s; the library's product with one scale for a whole
+// matrix 359), the matrix cores busy 68% of the cycles at 1.63 GHz; 16384 rows on 32 groups
+// of 4096 x 4096 292 us.  Dealing the groups' tiles out by height, tallest first, evened the
+// workgroups' rows and cost what they share in the L2: 305 -> 323 us.
 struct F8Large {
     // Codes: 32 KB a slot for A, then for B (a slot and block fit a read's offset field);
     // scales: 4 KB a window for A's rows and 1 KB for B's; 1 KB that nobody reads; what
@@ -474,7 +484,7 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_block_large_kernel(F8Args g, 
         for (int c = 0; c < 4; ++c) copy_b(c, k);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            if (c < fm) copy_a(c, k);
+            if (c < fm && (k == 0 || c < 2)) copy_a(c, k);  // the second stage's others: in the first
     };
 
     int v = blockIdx.x;
@@ -522,7 +532,7 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_block_large_kernel(F8Args g, 
             for (int j = 0; j < FM; ++j) to[j] = *reinterpret_cast<const float *>(base + (32 * (wm * FM + j) + r32) * 16) * sb;
         };
 
-        wait_vmcnt<4 + FM>();
+        wait_vmcnt<4 + (FM < 2 ? FM : 2)>();
         lds_barrier();
 #pragma unroll
         for (int q = 0; q < 4; ++q) read_a(fa[0], q, 0, 0);
@@ -563,11 +573,10 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_block_large_kernel(F8Args g, 
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int r = 8; r < 16; ++r) acc[pi][pj][r] = __builtin_fmaf(p[pi][r], ps, acc[pi][pj][r]);
-                    if (FM == 2 ? j == 0 && i == 1 : j == 1 && FM > 2) {
+                    if (FM > 2 && j == 0 && 2 + i < FM) copy_a(2 + i, k + 1);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if (FM == 2 || c / 2 == i) copy_b(c, k + 2);
-                    }
+                    for (int c = 0; c < 4; ++c)
+                        if (FM == 4 ? j == 1 + c / 2 && i == c % 2 : FM == 3 ? j == 1 && i == c / 2 : FM == 2 && j == 0 && i == 1) copy_b(c, k + 2);
                     if (last) {
                         read_b(i, 1 - ODD);
                         if (i == 0) {
@@ -578,7 +587,7 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_block_large_kernel(F8Args g, 
                         }
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            if (c < FM && c / 2 == i) copy_a(c, k + 2);
+                            if (c < FM && c < 2 && c == i) copy_a(c, k + 2);
                             if (FM == 1 && c / 2 == i) copy_b(c, k + 2);
                         }
                     }
