@@ -175,18 +175,28 @@ lpgemm_status launch_narrow_any(const F8Args &g, const NarrowPlan &p, hipStream_
 //     200 x 8582 x 6277    36.4 / 34.0 / 64.0     513 x 6086 x 384     10.2 /  8.1 /    -
 // 32 groups of 4096 x 4096, rows shared out by chance:
 //     1024 rows  111 / 121 / 129    4096 rows  223 / 157 / 142    16384 rows  646 / 403 / 296
+// Binary32 results convert codes on the vector ALU and have costs of their own (64 x 64 /
+// 128 x 128):
+//     512 x 2048 x 4096    15.7 / 37.3    1500 x 1500 x 1500   17.7 / 19.6
+//     1024 x 2048 x 512     7.8 / 10.9    2048 x 2048 x 256    12.2 / 10.7
+//     2048 x 2048 x 2048   28.3 / 24.4    1024 x 4096 x 4096   49.9 / 41.6
+//     513 x 6086 x 384     13.4 / 12.0    4096 x 4096 x 4096    193 / 156
+// and 256 x 4096 x 4096, 64 x 64 whole / in two halves: 18.7 / 16.4, bf16 14.0 / 12.4.
 struct Shape {
     int high, wide, lds;
     double stage[4], few, tile;
 };
 enum { kShape64, kShape64Split, kShape128, kShape128Deep, kShape256, kShapeCount };
-Shape shape_of(int shape, int groups)
+Shape shape_of(int shape, int groups, int format)
 {
+    const bool f32 = format == OUT_F32;
     switch (shape) {
-    case kShape64: return {64, 64, F8Tile<1, 1, 4>::lds(groups, 1), {0.26}, 0.34, 1.5};
-    case kShape64Split: return {64, 64, F8Tile<1, 1, 4>::lds(groups, 2), {0.26}, 0.26, 2.5};
+    case kShape64: return {64, 64, F8Tile<1, 1, 4>::lds(groups, 1), {f32 ? 0.36 : 0.26}, f32 ? 0.38 : 0.34, 1.5};
+    case kShape64Split: return {64, 64, F8Tile<1, 1, 4>::lds(groups, 2), {f32 ? 0.30 : 0.22}, f32 ? 0.30 : 0.26, 2.5};
     case kShape128: return {128, 128, F8Tile<2, 2, 2>::lds(groups, 1), {0.45, 0.60}, 0.72, 2.0};
-    case kShape128Deep: return {128, 128, F8Tile<2, 2, 4>::lds(groups, 1), {0.50, 0.72}, 0.72, 2.0};
+    case kShape128Deep:
+        if (f32) return {128, 128, F8Tile<2, 2, 4>::lds(groups, 1), {0.70, 0.98}, 0.98, 6.0};
+        return {128, 128, F8Tile<2, 2, 4>::lds(groups, 1), {0.50, 0.72}, 0.72, 2.0};
     default: return {256, 256, F8Large::lds(groups), {0.85, 1.10, 1.40, 1.72}, 1.40, 4.0};
     }
 }
@@ -194,11 +204,13 @@ constexpr int kSplitUnits = 16;       // two windows of scales for each half
 constexpr double kMemory = 4.9e6;     // bytes of matrices a us, whatever the shape
 
 // Which results and scales a shape has: the large kernel's K loop has registers for one
-// scale a tile's columns and 16-bit results alone; a scale for every row of B takes 64 x 64.
+// scale a tile's columns and 16-bit results alone; a scale for every row of B takes 64 x 64;
+// binary32 results' 128 x 128 take more registers than two workgroups have, so one with
+// the deeper ring (4096^3 172 us as two that spill, 1024 x 4096 x 4096 61 -> 42).
 bool serves(const F8Args &g, int format, int shape)
 {
     if (shape == kShape256) return format != OUT_F32 && g.sb_shift != 0 && g.U >= F8Large::kMinUnits;
-    return shape == kShape64 || (shape == kShape64Split ? g.U >= kSplitUnits : g.sb_shift != 0);
+    return shape == kShape64 || (shape == kShape64Split ? g.U >= kSplitUnits : g.sb_shift != 0 && (shape == kShape128Deep || format != OUT_F32));
 }
 
 int64_t tiles_of(const F8Args &g, const Shape &s, int64_t *blocks)
@@ -217,11 +229,11 @@ int choose_shape(const F8Args &g, int format, int64_t cu, double *time)
     *time = 0;
     for (int i = 0; i < kShapeCount; ++i) {
         if (!serves(g, format, i)) continue;
-        const Shape s = shape_of(i, 0);
+        const Shape s = shape_of(i, 0, format);
         int64_t blocks;
         const int64_t tiles = tiles_of(g, s, &blocks);
         // one tile to a compute unit: K in two halves, a ring of four stages
-        if ((i == kShape64Split || i == kShape128Deep) && tiles > cu) continue;
+        if ((i == kShape64Split || (i == kShape128Deep && serves(g, format, kShape128))) && tiles > cu) continue;
         if (i == kShape128 && tiles <= cu) continue;
         const double stage = tiles < cu * 3 / 4 ? std::min(s.few, s.stage[blocks - 1] * 1.3) : s.stage[blocks - 1];
         const double own = (double)ceil_div(tiles, cu) * ((double)g.U * stage + s.tile);
@@ -256,9 +268,9 @@ struct F8Plan {
     int threads;
 };
 
-lpgemm_status plan_shape(const F8Args &g, int shape, int64_t cu, F8Plan *p)
+lpgemm_status plan_shape(const F8Args &g, int format, int shape, int64_t cu, F8Plan *p)
 {
-    const Shape s = shape_of(shape, g.E);
+    const Shape s = shape_of(shape, g.E, format);
     const int64_t tiles_n = ceil_div(g.N, s.wide);
     // 32-bit tile counts; at most one ragged row tile a group more than the rows fill
     if (ceil_div(g.R, s.high) + g.E > INT32_MAX / tiles_n) return LPGEMM_ERR_UNSUPPORTED;
@@ -279,16 +291,17 @@ lpgemm_status plan_product(const F8Args &g, int format, int64_t cu, int forced, 
     case LPGEMM_KERNEL_TILED: {
         if (forced == LPGEMM_KERNEL_AUTO && narrow_serves(g) && narrow_pays(g, cu)) return narrow();
         double time;
-        return plan_shape(g, choose_shape(g, format, cu, &time), cu, p);
+        return plan_shape(g, format, choose_shape(g, format, cu, &time), cu, p);
     }
     case LPGEMM_KERNEL_TILED_256:
-        if (serves(g, format, kShape256)) return plan_shape(g, kShape256, cu, p);
+        if (serves(g, format, kShape256)) return plan_shape(g, format, kShape256, cu, p);
         [[fallthrough]];
     case LPGEMM_KERNEL_TILED_128:
-        if (serves(g, format, kShape128)) return plan_shape(g, g.R * (int64_t)g.N > 128 * 128 * cu ? kShape128 : kShape128Deep, cu, p);
+        if (serves(g, format, kShape128Deep))
+            return plan_shape(g, format, g.R * (int64_t)g.N > 128 * 128 * cu && serves(g, format, kShape128) ? kShape128 : kShape128Deep, cu, p);
         [[fallthrough]];
     case LPGEMM_KERNEL_TILED_64:
-        return plan_shape(g, g.R * (int64_t)g.N > 64 * 64 * cu || !serves(g, format, kShape64Split) ? kShape64 : kShape64Split, cu, p);
+        return plan_shape(g, format, g.R * (int64_t)g.N > 64 * 64 * cu || !serves(g, format, kShape64Split) ? kShape64 : kShape64Split, cu, p);
     case LPGEMM_KERNEL_SKINNY: return narrow_serves(g) ? narrow() : LPGEMM_ERR_UNSUPPORTED;
     default: return LPGEMM_ERR_UNSUPPORTED;
     }
@@ -304,7 +317,9 @@ lpgemm_status launch_product(const F8Args &g, hipStream_t stream)
     switch (p.shape) {
     case kShape64: return rows ? launch_tiled<1, 1, 4, 1, true, OUT>(g, p.blocks, stream) : launch_tiled<1, 1, 4, 1, false, OUT>(g, p.blocks, stream);
     case kShape64Split: return rows ? launch_tiled<1, 1, 4, 2, true, OUT>(g, p.blocks, stream) : launch_tiled<1, 1, 4, 2, false, OUT>(g, p.blocks, stream);
-    case kShape128: return launch_tiled<2, 2, 2, 1, false, OUT>(g, p.blocks, stream);
+    case kShape128:
+        if constexpr (OUT != OUT_F32) return launch_tiled<2, 2, 2, 1, false, OUT>(g, p.blocks, stream);
+        return LPGEMM_ERR_UNSUPPORTED;
     case kShape128Deep: return launch_tiled<2, 2, 4, 1, false, OUT>(g, p.blocks, stream);
     case kShape256:
         if constexpr (OUT != OUT_F32) return launch_large<OUT>(g, p.blocks, stream);
@@ -425,7 +440,7 @@ lpgemm_status lpgemm_fp8_block_plan(int64_t R, int64_t N, int64_t K, int64_t E, 
     const lpgemm_status st = plan_product(g, OUT_BF16, cu_count > 0 ? cu_count : 256, forced_kernel(), &p);
     if (st != LPGEMM_OK) return st;
     const bool narrow = p.shape == kShapeCount;
-    const Shape s = shape_of(p.shape, 0);
+    const Shape s = shape_of(p.shape, 0, OUT_BF16);
     info->kernel = narrow ? LPGEMM_KERNEL_SKINNY : LPGEMM_KERNEL_TILED;
     info->tile_m = !narrow ? s.high : p.narrow.ring || R <= 16 ? 16 : 32;
     info->tile_n = narrow ? 16 : s.wide;

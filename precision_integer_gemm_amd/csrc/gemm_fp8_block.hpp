@@ -105,9 +105,10 @@ struct F8Tile {
 
 // KG == 2: eight waves, the second four on the second half of K with a ring of their
 // own; their sums are added at the end, through LDS.
-// ROWS: B has a scale for every row.
+// ROWS: B has a scale for every row.  Binary32 results' larger tiles keep their codes' bf16
+// forms too, in twice the registers: one workgroup to a compute unit.
 template <int HM, int FN, int STAGES, int KG, bool ROWS, int OUT>
-__global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void gemm_fp8_block_tiled_kernel(F8Args g, int tiles_n, int xcds)
+__global__ __launch_bounds__(256 * KG, KG == 1 && !(OUT == OUT_F32 && HM == 2) ? 2 : 1) void gemm_fp8_block_tiled_kernel(F8Args g, int tiles_n, int xcds)
 {
     using T = F8Tile<HM, FN, STAGES>;
     static_assert(4 * mx_stage_bytes<OUT, FN>() <= T::kStages * T::kCodes, "the ring holds the rows on their way out");
