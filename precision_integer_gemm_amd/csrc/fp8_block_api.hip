@@ -24,10 +24,14 @@ lpgemm_status check_values(const void *x, const void *codes, const void *scales,
     return LPGEMM_OK;
 }
 
-// Items of a thread: four where that leaves four workgroups a compute unit, else one.
-constexpr int64_t kManyItems = 4 * 256 * 4 * 256;
+// Codes back to values: from so many items on, four a thread, and values that pass by the
+// caches (us, one kept / four past: 1001 x 2897 bf16 3.25 / 3.57, 1024 x 4096 bf16 3.65 /
+// 3.21, 2048 x 4096 bf16 5.75 / 4.12, 8192 x 8192 fp32 67.9 / 48.5).
+constexpr int64_t kManyItems = 2 * 256 * 4 * 256;
 // Values of more bytes than this do not stay in the 256 MB last-level cache
-// between a call and the next: they pass by it.
+// between a call and the next: to codes, they pass by it (us, kept / past: a scale per row,
+// 4096 x 4096 fp32 13.3 / 16.0, 16384 x 8192 bf16 72.3 / 70.8; per 128 rows 14.2 / 16.8,
+// 72.8 / 62.7, 8192 x 8192 fp32 59.4 / 57.3).
 constexpr int64_t kPastCaches = 192 << 20;
 
 template <int IN, bool POW2>
@@ -43,9 +47,8 @@ lpgemm_status launch_quantize(const void *x, int64_t ldx, uint8_t *codes, float 
                                scales + first * units, rows - 128 * first, (int32_t)K, (uint32_t)units);
         });
     }
-    const bool many = rows * items >= kManyItems;
-    const auto kernel = past ? &fp8_block_quantize_kernel<IN, 4, true, POW2> : many ? &fp8_block_quantize_kernel<IN, 4, false, POW2> : &fp8_block_quantize_kernel<IN, 1, false, POW2>;
-    return launch_rows(rows, items, past || many ? 1024 : 256, [&](int64_t first, int64_t count, dim3 blocks) {
+    const auto kernel = past ? &fp8_block_quantize_kernel<IN, true, POW2> : &fp8_block_quantize_kernel<IN, false, POW2>;
+    return launch_rows(rows, items, 256, [&](int64_t first, int64_t count, dim3 blocks) {
         hipLaunchKernelGGL(kernel, blocks, dim3(256), 0, stream, static_cast<const uint8_t *>(x) + first * ldx * width, ldx, to + first * items,
                            scales + first * units, count, (int32_t)K, (uint32_t)items);
     });
@@ -62,9 +65,8 @@ lpgemm_status launch_dequantize(const uint8_t *codes, const float *scales, int s
 {
     const int64_t items = units_of(K) * (kF8Unit / f8_item<OUT>()), width = (int64_t)element_bytes(OUT);
     const bool many = rows * items >= kManyItems;
-    const bool past = rows * K * width > kPastCaches / 2;
-    const auto kernel = past ? &fp8_block_dequantize_kernel<OUT, 4, true> : many ? &fp8_block_dequantize_kernel<OUT, 4, false> : &fp8_block_dequantize_kernel<OUT, 1, false>;
-    return launch_rows(rows, items, past || many ? 1024 : 256, [&](int64_t first, int64_t count, dim3 blocks) {
+    const auto kernel = many ? &fp8_block_dequantize_kernel<OUT, 4, true> : &fp8_block_dequantize_kernel<OUT, 1, false>;
+    return launch_rows(rows, items, many ? 1024 : 256, [&](int64_t first, int64_t count, dim3 blocks) {
         hipLaunchKernelGGL(kernel, blocks, dim3(256), 0, stream, reinterpret_cast<const uint32_t *>(codes + first * items * f8_item<OUT>()), scales,
                            static_cast<uint8_t *>(y) + first * K * width, first, count, (int32_t)K, (uint32_t)items, shift);
     });
@@ -223,10 +225,10 @@ int64_t tiles_of(const F8Args &g, const Shape &s, int64_t *blocks)
 }
 
 // The shape that should take the least time; the smaller of equal ones.
-int choose_shape(const F8Args &g, int format, int64_t cu, double *time)
+int choose_shape(const F8Args &g, int format, int64_t cu)
 {
     int best = kShape64;
-    *time = 0;
+    double best_time = 0;
     for (int i = 0; i < kShapeCount; ++i) {
         if (!serves(g, format, i)) continue;
         const Shape s = shape_of(i, 0, format);
@@ -238,9 +240,9 @@ int choose_shape(const F8Args &g, int format, int64_t cu, double *time)
         const double stage = tiles < cu * 3 / 4 ? std::min(s.few, s.stage[blocks - 1] * 1.3) : s.stage[blocks - 1];
         const double own = (double)ceil_div(tiles, cu) * ((double)g.U * stage + s.tile);
         const double t = std::max(own, (double)std::min(g.E, g.R) * g.N * g.U * kF8UnitCodes / kMemory);
-        if (*time == 0 || t < *time) {
+        if (best_time == 0 || t < best_time) {
             best = i;
-            *time = t;
+            best_time = t;
         }
     }
     return best;
@@ -288,11 +290,9 @@ lpgemm_status plan_product(const F8Args &g, int format, int64_t cu, int forced, 
     };
     switch (forced) {
     case LPGEMM_KERNEL_AUTO:
-    case LPGEMM_KERNEL_TILED: {
+    case LPGEMM_KERNEL_TILED:
         if (forced == LPGEMM_KERNEL_AUTO && narrow_serves(g) && narrow_pays(g, cu)) return narrow();
-        double time;
-        return plan_shape(g, format, choose_shape(g, format, cu, &time), cu, p);
-    }
+        return plan_shape(g, format, choose_shape(g, format, cu), cu, p);
     case LPGEMM_KERNEL_TILED_256:
         if (serves(g, format, kShape256)) return plan_shape(g, format, kShape256, cu, p);
         [[fallthrough]];

@@ -79,39 +79,31 @@ __device__ __forceinline__ uint64_t f8_codes(const u32x4 (&w)[2], float inverse)
     return (uint64_t)c[1] << 32 | c[0];
 }
 
-// One row to a block.  A workgroup takes 256 J items of eight values, as in
-// mxfp4_quantize_kernel; 16 neighbouring lanes share a block.  `items` = 16 units
-// of a row.
-template <int IN, int J, bool NT, bool POW2>
+// One row to a block.  A workgroup takes 256 items of eight values; 16 neighbouring lanes
+// share a block.  `items` = 16 units of a row.  Bound by memory: 8192 x 8192 fp32 57.8 us
+// (5.8 TB/s), bf16 37.3; four items a thread took 60.9 and 39.7, 1001 x 2897 fp32 3.8 for 3.2.
+template <int IN, bool NT, bool POW2>
 __global__ __launch_bounds__(256) void fp8_block_quantize_kernel(const void *__restrict__ X, int64_t ldx, uint64_t *__restrict__ codes,
                                                                  float *__restrict__ scales, int64_t rows, int32_t K, uint32_t items)
 {
     const int64_t total = rows * items;  // a multiple of 16
-    const int64_t first = (int64_t)blockIdx.x * (256 * J);
+    const int64_t first = (int64_t)blockIdx.x * 256, i = first + threadIdx.x;
     const int64_t row0 = first / items;
-    const uint32_t rest0 = (uint32_t)(first - row0 * items);
-    u32x4 w[J][2];
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-        const uint32_t local = 256 * j + threadIdx.x;
-        const MxItem it = mx_item(row0, rest0 + local, items);
-        mx_load8<IN, NT>(X, it.row * ldx + it.k0, first + local < total ? K - it.k0 : 0, w[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-        const int64_t i = first + 256 * j + threadIdx.x;
-        float scale, inverse;
-        const bool fine = f8_scale<POW2>(f8_value<IN>(f8_largest16(mx_largest<IN>(w[j]))), scale, inverse);
-        const uint64_t c = fine ? f8_codes<IN>(w[j], inverse) : 0u;
-        if (i < total) {
-            codes[i] = c;
-            if ((i & 15) == 0) scales[i >> 4] = scale;
-        }
+    const MxItem it = mx_item(row0, (uint32_t)(first - row0 * items) + threadIdx.x, items);
+    u32x4 w[2];
+    mx_load8<IN, NT>(X, it.row * ldx + it.k0, i < total ? K - it.k0 : 0, w);
+    float scale, inverse;
+    const bool fine = f8_scale<POW2>(f8_value<IN>(f8_largest16(mx_largest<IN>(w))), scale, inverse);
+    const uint64_t c = fine ? f8_codes<IN>(w, inverse) : 0u;
+    if (i < total) {
+        codes[i] = c;
+        if ((i & 15) == 0) scales[i >> 4] = scale;
     }
 }
 
 // 128 rows to a block: a workgroup takes one block, 16 lanes to a row's 128
-// values, and holds it in registers between the maximum and the codes.
+// values, and holds it in registers between the maximum and the codes.  Bound by memory:
+// 8192 x 8192 fp32 57.3 us (5.9 TB/s).
 template <int IN, bool NT, bool POW2>
 __global__ __launch_bounds__(256) void fp8_block_quantize_square_kernel(const void *__restrict__ X, int64_t ldx, uint64_t *__restrict__ codes,
                                                                         float *__restrict__ scales, int64_t rows, int32_t K, uint32_t units)
@@ -144,7 +136,8 @@ __global__ __launch_bounds__(256) void fp8_block_quantize_square_kernel(const vo
 
 // Codes back to values: fl(e4m3 * s), rounded to OUT.  Items of V codes, four
 // where a value takes four bytes, so that a store instruction writes whole
-// lines (with eight a lane it wrote half of every 32 bytes).
+// lines (with eight a lane it wrote half of every 32 bytes).  Bound by the stores: 8192 x
+// 8192 to fp32 48.5 us (6.9 TB/s), to bf16 30.1.
 // `shift`: 0, or 7 where 128 rows share a scale.
 template <int OUT>
 constexpr int f8_item() { return OUT == OUT_F32 ? 4 : 8; }

@@ -372,6 +372,11 @@ __host__ __device__ inline int route_lds(int E, int top, bool room)
 
 // Chooses every token's experts; with one workgroup (`alone`, one round) the lists too,
 // else each workgroup's counts.  `per`: tokens of a wave in a round.
+//
+// Bound by instructions, for few tokens by their chain: one token of 256 experts, top 8 of
+// 4 groups of 8, sigmoids with a bias 7.6 us; 512 tokens of 64, softmax 6.1; 8192 of 256
+// 21.0 (the logits take 1.6 to read).  64 registers for two workgroups a compute unit
+// spill: 24 to 32.
 template <int IN, int V, bool WIDE>
 __global__ __launch_bounds__(kRouteThreads, 4) void route_choose_kernel(RouteArgs g, int per, int alone)
 {
@@ -434,7 +439,8 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_choose_kernel(RouteArg
     for (int i = tid; i < g.E; i += kRouteThreads) g.counts[(int64_t)blockIdx.x * route_pitch(g.E) + i] = (uint16_t)count[i];
 }
 
-// The lists from the workgroups' counts: each adds up those of the ones before it.
+// The lists from the workgroups' counts: each adds up those of the ones before it (512
+// tokens 5.2 us, 8192 7.0; from 512 workgroups' counts 10.8): bound by the chain of loads.
 __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs g)
 {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -507,6 +513,8 @@ __global__ __launch_bounds__(256) void route_empty_kernel(int32_t *offsets, int3
 //   dL / dp_k = scale (g_k - sum_j g_j w'_j) / S  or  scale g_k;  0 for the others
 //   softmax: dx_i = p_i (dp_i - sum_j p_j dp_j);  sigmoid: dx_i = p_i (1 - p_i) dp_i
 // The renormalised softmax has sum p dp = 0 and a gradient at the chosen alone.
+// One wave to a token: 8192 x 256 fp32 9.5 us (1.8 TB/s), a row's loads, exponentials and
+// two sums over the wave one after another.
 struct RouteGradArgs {
     const void *logits;
     const float *dweights;   // [T][top]
@@ -640,7 +648,7 @@ __device__ __forceinline__ void route_store8(void *y, int64_t at, int n, int N, 
 }
 
 // A workgroup takes J pieces of 2048 values of a row.  NT: rows that no cache will keep
-// pass by them.
+// pass by them.  8192 tokens of 4 rows of 4096 bf16 59 us (5.7 TB/s); 16 of 4 2.8.
 template <int IN, int OUT, int J, bool NT>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs g)
 {
@@ -689,7 +697,8 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs g)
 }
 
 // dy[places[t][k]] = weights[t][k] dout[t];  dweights[t][k] = <dout[t], y[places[t][k]]>.
-// A workgroup takes a token; binary32 sums in a fixed order.
+// A workgroup takes a token; binary32 sums in a fixed order.  Bound by memory: 8192 tokens
+// of 4 rows of 4096 bf16 116 us (5.2 TB/s).
 struct CombineGradArgs {
     const void *dout;       // [T][N]
     const void *y;          // [R][N]

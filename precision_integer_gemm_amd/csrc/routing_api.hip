@@ -26,9 +26,11 @@ RoutePlan plan_route(int64_t T)
 }
 
 // Rows of more bytes than this do not stay in the 256 MB last-level cache between a call
-// and the next: the sum's loads pass by it (8192 x 4 rows of 4096 bf16, 268 MB: 77 us kept,
-// 64 passed by; the gradients, which write as much: 116 and 126, so they are kept).
-constexpr int64_t kPastCaches = 192 << 20;
+// and the next: the sum's loads pass by it, with two pieces of a long row to a workgroup
+// (us, kept / past, bf16: 2048 tokens of 4 rows of 4096 16.4 / 17.3, 4096 34.1 / 31.3, 8192
+// 78.7 / 59.1; of 2048, 4096 tokens of 8 27.6 / 29.4, 16384 of 4 79.3 / 63.1).  The
+// gradients write as much as they read: 8192 of 4 of 4096 116 kept, 126 past.
+constexpr int64_t kPastCaches = 96 << 20;
 
 size_t route_workspace(int64_t T, int64_t E)
 {
@@ -108,11 +110,10 @@ lpgemm_status launch_backward(const RouteGradArgs &g, hipStream_t stream)
 template <int IN>
 lpgemm_status launch_combine(CombineArgs g, int out, hipStream_t stream)
 {
-    const bool two = g.N > 2048 && g.T >= 1024;  // long rows of many tokens: more loads in flight
-    const bool past = two && g.R * g.N * (int64_t)element_bytes(IN) > kPastCaches;
+    const bool past = g.R * g.N * (int64_t)element_bytes(IN) > kPastCaches, two = past && g.N > 2048;
     const auto pick = [&](auto type) {
         constexpr int OUT = decltype(type)::value;
-        return past ? &combine_kernel<IN, OUT, 2, true> : two ? &combine_kernel<IN, OUT, 2, false> : &combine_kernel<IN, OUT, 1, false>;
+        return two ? &combine_kernel<IN, OUT, 2, true> : past ? &combine_kernel<IN, OUT, 1, true> : &combine_kernel<IN, OUT, 1, false>;
     };
     const auto kernel = out == OUT_F32    ? pick(std::integral_constant<int, OUT_F32>{})
                         : out == OUT_BF16 ? pick(std::integral_constant<int, OUT_BF16>{})
