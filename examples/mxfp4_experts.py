@@ -2,11 +2,11 @@
 
     python examples/mxfp4_experts.py [tokens]
 
-Weights are quantised once, as when a model is loaded.  A step quantises the
-tokens' hidden states, multiplies each expert's rows with its up projection,
-applies the activation, quantises again, multiplies with the down projection
-and adds a token's experts up; a shared expert takes every token through the
-plain product.  The result is set against the same layer in float32.
+Weights are quantised once, as when a model is loaded.  A step routes the tokens,
+quantises their hidden states, multiplies each expert's rows with its up
+projection, applies the activation, quantises again, multiplies with the down
+projection and adds a token's experts up; a shared expert takes every token through
+the plain product.  The result is set against the same layer in float32.
 """
 import os
 import sys
@@ -25,35 +25,25 @@ def quantised(w):
     return codes.view(*w.shape[:-1], -1), scales.view(*w.shape[:-1], -1)
 
 
-def route(x, router):
-    """(rows, offsets, weights, token): the tokens of every expert in turn."""
-    weight, chosen = (x.float() @ router.t()).softmax(1).topk(TOP, 1)
-    order = chosen.flatten().argsort(stable=True)
-    sizes = torch.bincount(chosen.flatten(), minlength=EXPERTS)
-    offsets = torch.cat((sizes.new_zeros(1), sizes.cumsum(0))).int()
-    token = order // TOP
-    return token.int(), offsets, weight.flatten()[order], token
-
-
 def layer(x, router, up, down, shared):
-    rows, offsets, weight, token = route(x, router)
+    r = L.lpgemm_route(x.float() @ router.t(), TOP, renormalise=False)
     a, sa = L.lpgemm_mxfp4_quantize(x)
-    h = L.lpgemm_mxfp4_grouped(a, sa, *up, offsets, rows=rows)  # [tokens * TOP, INNER]
+    h = L.lpgemm_mxfp4_grouped(a, sa, *up, r.offsets, rows=r.rows)  # [tokens * TOP, INNER]
     h = torch.nn.functional.silu(h)
-    y = L.lpgemm_mxfp4_grouped(*L.lpgemm_mxfp4_quantize(h), *down, offsets, dtype=torch.float32)
+    y = L.lpgemm_mxfp4_grouped(*L.lpgemm_mxfp4_quantize(h), *down, r.offsets, dtype=torch.float32)
     out = L.lpgemm_mxfp4(a, sa, *shared, dtype=torch.float32)
-    return out.index_add_(0, token, y * weight[:, None])
+    return L.lpgemm_combine(y, r.places, r.weights, residual=out)
 
 
 def plain(x, router, up, down, shared):
     """The same layer on float32 weights."""
-    rows, offsets, weight, token = route(x, router)
     x = x.float()
-    out, at = x @ shared.t(), offsets.tolist()
+    weight, chosen = (x @ router.t()).softmax(1).topk(TOP, 1)
+    out = x @ shared.t()
     for e in range(EXPERTS):
-        i = slice(at[e], at[e + 1])
-        h = torch.nn.functional.silu(x[token[i]] @ up[e].t())
-        out.index_add_(0, token[i], (h @ down[e].t()) * weight[i, None])
+        token, k = torch.where(chosen == e)
+        h = torch.nn.functional.silu(x[token] @ up[e].t())
+        out.index_add_(0, token, (h @ down[e].t()) * weight[token, k, None])
     return out
 
 
