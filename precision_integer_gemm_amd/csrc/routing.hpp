@@ -640,11 +640,21 @@ __device__ __forceinline__ void route_load8(const void *x, int64_t at, int left,
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = f8_element<IN>(w, j);
 }
-template <int OUT>
+template <int OUT, bool NT>
 __device__ __forceinline__ void route_store8(void *y, int64_t at, int n, int N, const float (&v)[8])
 {
-    mx_store4<OUT>(y, at, n, N, v[0], v[1], v[2], v[3]);
-    mx_store4<OUT>(y, at, n + 4, N, v[4], v[5], v[6], v[7]);
+    if (n + 8 > N) {
+        mx_store4<OUT>(y, at, n, N, v[0], v[1], v[2], v[3]);
+        mx_store4<OUT>(y, at, n + 4, N, v[4], v[5], v[6], v[7]);
+    } else if (OUT == OUT_F32) {
+        float *p = static_cast<float *>(y) + at + n;
+#pragma unroll
+        for (int i = 0; i < 8; i += 4)
+            mx_store16<NT>(p + i, u32x4{__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3])});
+    } else {
+        mx_store16<NT>(static_cast<uint16_t *>(y) + at + n,
+                       u32x4{mx_pack2<OUT>(v[0], v[1]), mx_pack2<OUT>(v[2], v[3]), mx_pack2<OUT>(v[4], v[5]), mx_pack2<OUT>(v[6], v[7])});
+    }
 }
 
 // A workgroup takes J pieces of 2048 values of a row.  NT: rows that no cache will keep
@@ -692,13 +702,14 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs g)
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum[q][i] += f8_element<OUT>(v, i);
         }
-        route_store8<OUT>(g.out, t * g.N, n, g.N, sum[q]);
+        route_store8<OUT, false>(g.out, t * g.N, n, g.N, sum[q]);
     }
 }
 
 // dy[places[t][k]] = weights[t][k] dout[t];  dweights[t][k] = <dout[t], y[places[t][k]]>.
-// A workgroup takes a token; binary32 sums in a fixed order.  Bound by memory: 8192 tokens
-// of 4 rows of 4096 bf16 116 us (5.2 TB/s).
+// A workgroup takes a token; binary32 sums in a fixed order.  NT as above.  Bound by memory:
+// 8192 tokens of 4 rows of 4096 bf16 116 us (5.2 TB/s).  One row at a time: with four rows'
+// loads ahead, and the registers for them, 128 to 143.
 struct CombineGradArgs {
     const void *dout;       // [T][N]
     const void *y;          // [R][N]
@@ -712,7 +723,7 @@ struct CombineGradArgs {
 
 constexpr int kCombineSlots = 8;  // experts at a time
 
-template <int IN, int OUT>
+template <int IN, int OUT, bool NT>
 __global__ __launch_bounds__(256) void combine_backward_kernel(CombineGradArgs g)
 {
     __shared__ float part[4][kCombineSlots];
@@ -736,13 +747,14 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(CombineGradArgs g
             for (int j = 0; j < kCombineSlots; ++j) {
                 if (at[j] < 0) continue;
                 float v[8];
-                route_load8<IN>(g.y, (int64_t)at[j] * g.N + n, g.N - n, v);
+                u32x4 y[2];
+                mx_load8<IN, NT>(g.y, (int64_t)at[j] * g.N + n, g.N - n, y);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    dot[j] = __builtin_fmaf(d[i], v[i], dot[j]);
+                    dot[j] = __builtin_fmaf(d[i], f8_element<IN>(y, i), dot[j]);
                     v[i] = w[j] * d[i];
                 }
-                route_store8<IN>(g.dy, (int64_t)at[j] * g.N, n, g.N, v);
+                route_store8<IN, NT>(g.dy, (int64_t)at[j] * g.N, n, g.N, v);
             }
         }
         __syncthreads();  // the last slots' sums have been read

@@ -29,7 +29,8 @@ RoutePlan plan_route(int64_t T)
 // and the next: the sum's loads pass by it, with two pieces of a long row to a workgroup
 // (us, kept / past, bf16: 2048 tokens of 4 rows of 4096 16.4 / 17.3, 4096 34.1 / 31.3, 8192
 // 78.7 / 59.1; of 2048, 4096 tokens of 8 27.6 / 29.4, 16384 of 4 79.3 / 63.1).  The
-// gradients write as much as they read: 8192 of 4 of 4096 116 kept, 126 past.
+// gradients' loads and stores do from twice that on (4096 of 4 of 4096 57.9 / 61.4, 8192
+// 131 / 116).
 constexpr int64_t kPastCaches = 96 << 20;
 
 size_t route_workspace(int64_t T, int64_t E)
@@ -133,9 +134,14 @@ lpgemm_status launch_combine(CombineArgs g, int out, hipStream_t stream)
 template <int IN>
 lpgemm_status launch_combine_backward(const CombineGradArgs &g, int out, hipStream_t stream)
 {
-    const auto kernel = out == OUT_F32    ? &combine_backward_kernel<IN, OUT_F32>
-                        : out == OUT_BF16 ? &combine_backward_kernel<IN, OUT_BF16>
-                                          : &combine_backward_kernel<IN, OUT_F16>;
+    const bool past = g.R * g.N * (int64_t)element_bytes(IN) > 2 * kPastCaches;
+    const auto pick = [&](auto type) {
+        constexpr int OUT = decltype(type)::value;
+        return past ? &combine_backward_kernel<IN, OUT, true> : &combine_backward_kernel<IN, OUT, false>;
+    };
+    const auto kernel = out == OUT_F32    ? pick(std::integral_constant<int, OUT_F32>{})
+                        : out == OUT_BF16 ? pick(std::integral_constant<int, OUT_BF16>{})
+                                          : pick(std::integral_constant<int, OUT_F16>{});
     return launch_rows(g.T, 1, 1, [&](int64_t first, int64_t, dim3 blocks) {
         CombineGradArgs a = g;
         a.dout = static_cast<const uint8_t *>(g.dout) + first * g.N * (out == OUT_F32 ? 4 : 2);
