@@ -893,7 +893,11 @@ def lpgemm_fp8_block_plan(R: int, N: int, K: int, E: int = 0, cu_count: int = 0)
 def _route_options(top, score, groups, top_groups, group_top, renormalise, scale):
     if score not in ROUTE_SCORES:
         raise ValueError(f"score must be one of {list(ROUTE_SCORES)}, got {score!r}")
-    return RouteOptions(ROUTE_SCORES[score], top, groups, groups if top_groups is None else top_groups, group_top, int(bool(renormalise)), scale)
+    sizes = {"top": top, "groups": groups, "top_groups": groups if top_groups is None else top_groups, "group_top": group_top}
+    for name, v in sizes.items():
+        if not -2 ** 31 <= v < 2 ** 31:  # the structure's fields would keep its low bits
+            raise ValueError(f"{name}={v} is out of range")
+    return RouteOptions(ROUTE_SCORES[score], *sizes.values(), int(bool(renormalise)), scale)
 
 
 def _route_logits(logits):

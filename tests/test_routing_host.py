@@ -130,3 +130,14 @@ class TestReference:
         assert R.route(x, 3, "sigmoid", groups=4, top_groups=2, group_top=2)[0].tolist() == [[0, 2, 3]]
         assert R.route(np.full((1, 4), -math.inf), 2)[0].tolist() == [[-1, -1]]
         assert R.route(np.array([[1.0, 1, 1, 1]]), 2)[0].tolist() == [[0, 1]]
+
+
+@pytest.mark.parametrize("name", ["top", "groups", "top_groups", "group_top"])
+@pytest.mark.parametrize("value", [2 ** 32 + 1, -2 ** 32 + 1, 2 ** 31])
+def test_sizes_past_the_options_fields(name, value):
+    from precision_integer_gemm_amd import _binding
+    given = {"top": 2, "score": "softmax", "groups": 4, "top_groups": 1, "group_top": 1, "renormalise": True, "scale": 1.0}
+    made = _binding._route_options(**given)
+    assert (made.top, made.groups, made.top_groups, made.group_top) == (2, 4, 1, 1)
+    with pytest.raises(ValueError, match=name):
+        _binding._route_options(**{**given, name: value})
