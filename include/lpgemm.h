@@ -655,8 +655,8 @@ lpgemm_status lpgemm_combine(const void *Y, lpgemm_out_dtype y_dtype, int64_t R,
  * fixed order; the residual's is dout.
  *   dout      device, out_dtype [T][N]
  *   dY        device, y_dtype [R][N]: rows in no place are left as they are.  No
- *             row may be in two places (lpgemm_route makes none): it would get
- *             one of the two gradients.
+ *             row may be in two places (lpgemm_route makes none): each of its
+ *             values would be either gradient's.
  *   dweights  device, float [T][top], written whole
  * Errors as for lpgemm_combine.
  */

@@ -7,9 +7,10 @@ kernel), csrc/mxfp4_api.hip (the microscaled 4-bit kernels),
 csrc/fp8_block_api.hip (e4m3 with block scales) and csrc/routing_api.hip
 (experts' routing) with hipcc into precision_integer_gemm_amd/_lpgemm.so, next
 to this file, and the measurement probe csrc/ceiling_probe.hip into _ceiling.so
-(loaded only by bench.py).  These need hipcc alone.  Where PyTorch for ROCm, Python's headers and g++ are there,
-csrc/tensor_calls.cpp becomes the Python module _tensor_calls.so, the short way
-of the microscaled tensor calls; without it they take their longer way.
+(loaded only by bench.py).  These need hipcc alone.  Where PyTorch for ROCm,
+Python's headers and g++ are there, csrc/tensor_calls.cpp becomes the Python
+module _tensor_calls.so, the short way of the float operators' tensor calls;
+without it they take their longer way.
 """
 from __future__ import annotations
 
